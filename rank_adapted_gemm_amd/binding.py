@@ -26,12 +26,27 @@ EXPORTS = ("lora_proj", "lora_proj_ex", "lora_proj_multi", "lora_proj_sliced", "
            "lora_proj_workspace_bytes", "lora_proj_sliced_workspace_bytes", "lora_proj_q4_workspace_bytes",
            "lora_proj_path", "lora_proj_tile_rows", "lora_status_string", "lora_extract", "lora_extract_workspace_bytes",
            "lora_probe_mfma_bf16", "lora_probe_read", "lora_workspace_status", "lora_debug_handover_fault",
-           "lora_decode_plan_describe", "lora_proj_noalloc", "lora_proj_ranked")
+           "lora_decode_plan_describe", "lora_proj_noalloc", "lora_proj_ranked", "lora_kv_append", "lora_attn",
+           "lora_attn_workspace_bytes", "lora_kv_evict")
 NOALLOC_SCRATCH_BYTES = 64 << 20   # the device array lora_proj_noalloc uses instead of a workspace
 PLAN_FIELDS = ("MT", "nst", "nrs", "ntA", "ntW", "n_used", "GA", "GW", "smaxW", "off_cnt", "off_pa", "pa_bytes",
                "off_pw", "pw_bytes", "off_th", "t_bytes", "off_tl", "total")
 
 _lib = None
+
+
+class KVCacheStruct(ctypes.Structure):
+    """lora_kv_cache (lora_attn.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class KVBatchStruct(ctypes.Structure):
+    """lora_kv_batch (lora_attn.h)."""
+    _fields_ = [("q_starts", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("n_seq", ctypes.c_int32)]
 
 
 class LoraError(RuntimeError):
@@ -99,6 +114,15 @@ def load():
     lib.lora_decode_plan_describe.argtypes = [i64, i64, i64, i32, i32, ctypes.POINTER(i64), i32,
                                               ctypes.POINTER(i64), i32]
     lib.lora_decode_plan_describe.restype = i32
+    lib.lora_kv_append.argtypes = [vp, vp, vp, vp, i64, i64, ctypes.c_int, vp]
+    lib.lora_kv_append.restype = ctypes.c_int
+    lib.lora_attn.argtypes = [vp, vp, vp, i64, i64, i32, ctypes.c_int, ctypes.c_float, i32, i32, vp, vp, vp, i64,
+                              vp, sz, vp]
+    lib.lora_attn.restype = ctypes.c_int
+    lib.lora_attn_workspace_bytes.argtypes = [vp, vp, i32, i32, i32, i32]
+    lib.lora_attn_workspace_bytes.restype = sz
+    lib.lora_kv_evict.argtypes = [vp, vp, vp, i64, i32, i32, i32, vp, i64, vp, vp, vp]
+    lib.lora_kv_evict.restype = ctypes.c_int
     _lib = lib
     return lib
 

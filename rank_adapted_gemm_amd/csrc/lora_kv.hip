@@ -1,0 +1,249 @@
+// Rows into the paged cache (append) and out of it (evict).
+#include "lora_kv.h"
+
+namespace lora {
+namespace {
+
+// ---------------------------------------------------------------- append
+//
+// A copy with an indirection, bound by bytes: every new row is read once and
+// written once.  A block takes kAppendRows consecutive rows, looks their pages
+// up once, and streams their k and v in 16-byte pieces.
+constexpr int kAppendRows = 4;
+
+template <typename T>
+__device__ __forceinline__ u32x2 to_e4m3(const u32x4& raw, float scale) {
+  typedef T vec8 __attribute__((ext_vector_type(8)));
+  const vec8 x = __builtin_bit_cast(vec8, raw);
+  float f[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float v = float(x[e]) / scale;
+    f[e] = v > 448.0f ? 448.0f : (v < -448.0f ? -448.0f : v);   // NaN stays NaN
+  }
+  u32x2 r;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    int b = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * w], f[4 * w + 1], 0, false);
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * w + 2], f[4 * w + 3], b, true);
+    r[w] = uint32_t(b);
+  }
+  return r;
+}
+
+// T: the rows' type; F8: the cache holds e4m3 codes.
+template <typename T, bool F8>
+__global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
+  __shared__ int64_t base[kAppendRows];   // byte offset of a row's slot in the pool, -1 without a valid page
+  const int r0 = blockIdx.x * kAppendRows;
+  const int nr = min(kAppendRows, a.rows - r0);
+  if (int(threadIdx.x) < nr) {
+    const int row = r0 + threadIdx.x;
+    const int i = seq_of_row(a.s, row);
+    const int pos = a.s.kv_len[i] - a.s.q_start[i + 1] + row;
+    const int sub = pos >> 4, pg = page_of(a.c, sub);
+    const int page = a.s.table[i * a.s.table_stride + pg];
+    const int slot = (sub - pg * a.c.page_subs) * 16 + (pos & 15);
+    base[threadIdx.x] = page_ok(a.c, page) ? page * a.c.page_stride + int64_t(slot) * a.c.token_stride : -1;
+  }
+  __syncthreads();
+  const int per_head = a.c.dim / 8, per_row = per_head * a.c.kv_heads;
+  for (int u = threadIdx.x; u < 2 * per_row * nr; u += 256) {
+    const bool is_v = u >= per_row * nr;
+    const int w = is_v ? u - per_row * nr : u;
+    const int r = w / per_row, c = w - r * per_row;
+    const int h = c / per_head, e = (c - h * per_head) * 8;
+    if (base[r] < 0) continue;
+    const char* src = (is_v ? a.v : a.k) + (r0 + r) * a.row_stride + h * a.head_stride + e * 2;
+    char* dst = (is_v ? a.c.v : a.c.k) + base[r] + int64_t(h) * a.c.head_stride;
+    const u32x4 x = *reinterpret_cast<const u32x4*>(src);
+    if constexpr (F8)
+      *reinterpret_cast<u32x2*>(dst + e) = to_e4m3<T>(x, (is_v ? a.c.v_scale : a.c.k_scale)[h]);
+    else
+      *reinterpret_cast<u32x4*>(dst + 2 * e) = x;
+  }
+}
+
+// ---------------------------------------------------------------- evict
+
+// Order-preserving key of a weight: NaN lowest, -0 and +0 equal.
+__device__ __forceinline__ uint32_t mass_key(float m) {
+  if (m != m) return 0u;
+  const uint32_t u = __builtin_bit_cast(uint32_t, m + 0.0f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+constexpr int kSelThreads = 1024;
+constexpr int kSelWaves = kSelThreads / 64;
+
+// One block per (sequence, head): the threshold of the budget's heaviest
+// positions by radix selection, eight key bits a pass, then the kept positions
+// in order.
+__global__ __launch_bounds__(kSelThreads) void evict_select_kernel(EvictArgs a) {
+  __shared__ uint32_t hist[256];
+  __shared__ uint32_t sel[2];
+  __shared__ int wave_eq[kSelWaves], wave_keep[kSelWaves];
+  const int i = blockIdx.x / a.c.kv_heads;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int len = a.s.kv_len[i];
+  const float* m = a.mass + int64_t(blockIdx.x) * a.mass_cap;
+  int32_t* kept = a.kept + int64_t(blockIdx.x) * a.budget;
+  float* mout = a.mass_out ? a.mass_out + int64_t(blockIdx.x) * a.budget : nullptr;
+
+  if (len <= a.budget) {
+    for (int p = tid; p < a.budget; p += kSelThreads) {
+      kept[p] = p < len ? p : -1;
+      if (mout) mout[p] = p < len ? m[p] : 0.0f;
+    }
+    return;
+  }
+
+  const int lo = a.sinks, hi = len - a.recent;
+  uint32_t prefix = 0, mask = 0;
+  uint32_t k = uint32_t(a.budget - a.sinks - a.recent);   // still to take among keys that match the prefix
+  if (k > 0) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      if (tid < 256) hist[tid] = 0;
+      __syncthreads();
+      for (int p = lo + tid; p < hi; p += kSelThreads) {
+        const uint32_t key = mass_key(m[p]);
+        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+      }
+      __syncthreads();
+      if (tid < 64) {   // bins from the top: lane l holds bins 255 - 4 l .. 252 - 4 l
+        uint32_t c[4], sum = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum += (c[e] = hist[255 - 4 * tid - e]);
+        uint32_t before = sum;
+        for (int d = 1; d < 64; d <<= 1) {
+          const uint32_t o = __shfl_up(before, d);
+          if (tid >= d) before += o;
+        }
+        before -= sum;   // keys in higher lanes' bins
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (before < k && before + c[e] >= k) {
+            sel[0] = uint32_t(255 - 4 * tid - e);
+            sel[1] = k - before;
+          }
+          before += c[e];
+        }
+      }
+      __syncthreads();
+      prefix |= sel[0] << shift;
+      mask |= 255u << shift;
+      k = sel[1];
+    }
+  }
+  // keys above the prefix are kept, and the first k equal to it
+  const bool any = a.budget > a.sinks + a.recent;
+  int eq_seen = 0, out = 0;
+  for (int b = 0; b < len; b += kSelThreads) {
+    const int p = b + tid;
+    const float v = p < len ? m[p] : 0.0f;
+    const bool mid = p >= lo && p < hi;
+    const uint32_t key = mass_key(v);
+    const bool eq = any && mid && key == prefix;
+    const uint64_t eqb = __ballot(eq);
+    if (lane == 0) wave_eq[wave] = __popcll(eqb);
+    __syncthreads();
+    int rank = eq_seen, all_eq = 0;
+    for (int w = 0; w < kSelWaves; ++w) {
+      if (w < wave) rank += wave_eq[w];
+      all_eq += wave_eq[w];
+    }
+    const uint64_t below = (uint64_t(1) << lane) - 1;
+    rank += __popcll(eqb & below);
+    const bool keep = p < len && (!mid || (any && key > prefix) || (eq && uint32_t(rank) < k));
+    const uint64_t kb = __ballot(keep);
+    if (lane == 0) wave_keep[wave] = __popcll(kb);
+    __syncthreads();
+    int at = out, all = 0;
+    for (int w = 0; w < kSelWaves; ++w) {
+      if (w < wave) at += wave_keep[w];
+      all += wave_keep[w];
+    }
+    at += __popcll(kb & below);
+    if (keep) {
+      kept[at] = p;
+      if (mout) mout[at] = v;
+    }
+    eq_seen += all_eq;
+    out += all;
+    __syncthreads();
+  }
+}
+
+constexpr int kGatherRows = 64;
+
+// Copies kept rows to their new slots; blockIdx.y is (sequence, head).
+__global__ __launch_bounds__(256) void evict_gather_kernel(EvictArgs a, int elem_bytes, uint32_t nan_word) {
+  __shared__ int64_t src[kGatherRows], dst[kGatherRows];   // byte offsets; -1: no row, -2: source page invalid
+  const int i = blockIdx.y / a.c.kv_heads, h = blockIdx.y - i * a.c.kv_heads;
+  const int n = min(a.s.kv_len[i], a.budget);
+  const int s0 = blockIdx.x * kGatherRows;
+  if (s0 >= n) return;
+  if (threadIdx.x < kGatherRows) {
+    const int slot = s0 + threadIdx.x;
+    int64_t so = -1, to = -1;
+    if (slot < n) {
+      const int pos = a.kept[int64_t(blockIdx.y) * a.budget + slot];
+      const int ss = pos >> 4, sp = page_of(a.c, ss), ds = slot >> 4, dp = page_of(a.c, ds);
+      const int spage = a.s.table[i * a.s.table_stride + sp];
+      const int dpage = a.dst_table[i * a.dst_stride + dp];
+      const int64_t head = int64_t(h) * a.c.head_stride;
+      so = page_ok(a.c, spage)
+               ? spage * a.c.page_stride + int64_t((ss - sp * a.c.page_subs) * 16 + (pos & 15)) * a.c.token_stride + head
+               : -2;
+      if (page_ok(a.c, dpage))
+        to = dpage * a.c.page_stride + int64_t((ds - dp * a.c.page_subs) * 16 + (slot & 15)) * a.c.token_stride + head;
+    }
+    src[threadIdx.x] = so;
+    dst[threadIdx.x] = to;
+  }
+  __syncthreads();
+  const int per = a.c.dim * elem_bytes / 16;
+  for (int u = threadIdx.x; u < kGatherRows * per; u += 256) {
+    const int r = u / per, c = (u - r * per) * 16;
+    if (dst[r] < 0) continue;
+    u32x4 kx = {nan_word, nan_word, nan_word, nan_word}, vx = kx;
+    if (src[r] >= 0) {
+      kx = *reinterpret_cast<const u32x4*>(a.c.k + src[r] + c);
+      vx = *reinterpret_cast<const u32x4*>(a.c.v + src[r] + c);
+    }
+    *reinterpret_cast<u32x4*>(a.c.k + dst[r] + c) = kx;
+    *reinterpret_cast<u32x4*>(a.c.v + dst[r] + c) = vx;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_kv_append(const AppendArgs& a, int dtype, int cache_dtype, hipStream_t stream) {
+  const dim3 grid((a.rows + kAppendRows - 1) / kAppendRows), block(256);
+  if (cache_dtype != LORA_KV_E4M3)   // a plain copy: the 16-bit types move alike
+    hipLaunchKernelGGL((append_kernel<__bf16, false>), grid, block, 0, stream, a);
+  else if (dtype == LORA_KV_BF16)
+    hipLaunchKernelGGL((append_kernel<__bf16, true>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((append_kernel<_Float16, true>), grid, block, 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_evict(const EvictArgs& a, int cache_dtype, hipStream_t stream) {
+  const int pairs = a.s.n * a.c.kv_heads;
+  hipLaunchKernelGGL(evict_select_kernel, dim3(pairs), dim3(kSelThreads), 0, stream, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  int kept = 0;
+  for (int i = 0; i < a.s.n; ++i) {
+    const int n = a.s.kv_len[i] < a.budget ? a.s.kv_len[i] : a.budget;
+    kept = n > kept ? n : kept;
+  }
+  if (kept == 0) return hipSuccess;
+  const bool f8 = cache_dtype == LORA_KV_E4M3;
+  hipLaunchKernelGGL(evict_gather_kernel, dim3((kept + kGatherRows - 1) / kGatherRows, pairs), dim3(256), 0, stream, a,
+                     f8 ? 1 : 2, f8 ? 0x7F7F7F7Fu : 0x7FFF7FFFu);
+  return hipGetLastError();
+}
+
+}  // namespace lora
