@@ -1,0 +1,497 @@
+// Attention of single tokens (and few rows) over the paged cache, and the join
+// of items that share rows.
+//
+// Bound by the bytes of the keys and values.  A block takes the packed rows of
+// one sequence and key-value head (at most 32) and a run of its positions; its
+// four waves take 32 positions each in turn, every one through an LDS ring of
+// its own that DMA loads fill, so no wave waits for another before the end.  A
+// wave waits for a step's keys, multiplies, refills them, waits for its values,
+// multiplies and refills those: with 256-wide 16-bit rows the ring is one step
+// deep and half of a wave's 32 KiB are under way at any time.  S^T = K Q^T and
+// O^T = V^T P^T run on 16 x 16 x 32 MFMAs as in the prompts' kernel.  The waves
+// join in LDS; items that share rows leave sums in the workspace for the join.
+#include "lora_attn_core.h"
+
+namespace lora {
+namespace {
+
+constexpr int kStep = 1 << kDecodeUnitShift;
+constexpr int kWaves = 4;
+
+// Values of a fragment: lane's column d = db * 16 + (lane & 15) and the eight positions that its
+// registers of weights stand for: 4 (lane >> 4) + 0..3, and the same past 16.
+template <typename T, bool F8, int DIM>
+struct ValueReader16 {
+  using R = Row<F8, DIM>;
+  uint32_t base;
+  __device__ __forceinline__ explicit ValueReader16(int lane) {
+    const int qd = lane >> 4, j = lane & 15;
+    if constexpr (F8) {
+      const int ri = j >> 1, row = qd * 4 + (ri & 3) + (ri >> 2) * 16;
+      base = uint32_t(row * R::kBytes + (swizzle(row) << 4) + (j & 1) * 8);
+    } else {
+      const int row = qd * 4 + (j >> 2);
+      base = uint32_t(row * R::kBytes + ((((j & 3) >> 1) ^ swizzle(row)) << 4) + (j & 1) * 8);
+    }
+  }
+  __device__ static __forceinline__ int swizzle(int row) {
+    if constexpr (F8) {
+      const int far = (row >> 4) & 1;
+      return R::kChunks == 16 ? (row & 7) | far << 3
+                              : (R::kChunks == 8 ? ((row >> 1) & 3) | far << 2 : ((row >> 2) & 1) | far << 1);
+    } else {
+      return R::kChunks >= 16 ? (row & 7) << 1 : ((row >> 1) & 3) << 1;
+    }
+  }
+  __device__ __forceinline__ u32x4 read(uint32_t tile, int db) const {
+    if constexpr (F8) {
+      typedef int32_t i32x2 __attribute__((ext_vector_type(2)));
+      typedef __attribute__((address_space(3))) i32x2* p8;
+      const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(p8(uintptr_t(tile + (base ^ uint32_t(db * 16)))));
+      return __builtin_bit_cast(u32x4, from_e4m3<T>(uint32_t(w[0]), uint32_t(w[1])));
+    } else {
+      typedef __attribute__((address_space(3))) s16x4* p16;
+      const uint32_t at = tile + (base ^ uint32_t(db * 32));
+      const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(p16(uintptr_t(at))));
+      const u32x2 b =
+          __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(p16(uintptr_t(at + 16 * R::kBytes))));
+      return u32x4{a[0], a[1], b[0], b[1]};
+    }
+  }
+};
+
+// QT: 16-row columns of packed rows.  MASS: scores go to the workspace.
+template <typename T, bool F8, int DIM, int QT, bool MASS>
+__global__ __launch_bounds__(kWaves * 64, 1) void decode_kernel(AttnArgs a, AttnPart part) {
+  using R = Row<F8, DIM>;
+  using x8 = typename Vec<T>::x8;
+  constexpr int BM = QT * 16, KS = DIM / 32, DB = DIM / 16, STEP = kStep * R::kBytes;   // STEP: bytes of a step's keys
+  constexpr int NS = STEP >= 16384 ? 1 : (STEP >= 8192 ? 2 : 4);                        // steps in a wave's ring
+  constexpr int NL = 2 * R::kLoads;                                                     // loads of a step's keys
+  constexpr int RING = 2 * NS * STEP;
+  constexpr int JOIN = BM * (DIM + 4) * 4;                                              // a wave's outputs at the end
+  constexpr int WAVE_LDS = RING > JOIN ? RING : JOIN;
+  __shared__ __attribute__((aligned(1024))) char lds[kWaves * WAVE_LDS];
+  __shared__ float ml[kWaves][BM][2];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int qd = lane >> 4, col = lane & 15;
+  const int s = seq_of_item(part, blockIdx.x);
+  const AttnSeq sq = part.seq[s];
+  const int first = s == 0 ? 0 : part.seq[s - 1].item_end;
+  const int M = sq.rows * a.group;
+  const AttnItem item = attn_item(int(blockIdx.x) - first, a.c.kv_heads, sq.nsplit, 1);
+  const int t0 = sq.kv_len - sq.rows, t_lo = t0, t_hi = sq.kv_len - 1;
+  const Units units = units_of(t_lo, t_hi, a.window, a.sinks, kDecodeUnitShift);
+  const int u0 = split_begin(units.count, item.split, sq.nsplit);
+  const int nu = split_begin(units.count, item.split + 1, sq.nsplit) - u0;
+  const int mine = nu > wave ? (nu - wave + kWaves - 1) / kWaves : 0;   // the wave's steps: units wave, wave + 4, ...
+  const Pages pages = pages_of(a, sq.index, t_lo, t_hi);
+  const int lowx = a.window < 0 ? 0 : t_hi - a.window + 1;
+
+  const uint32_t ring = lds_addr(lds) + wave * WAVE_LDS;
+  const int lrow = lane / R::kChunks, lslot = lane % R::kChunks;
+  // loads of step i's keys or values: two 16-position groups
+  uint32_t ringbad = 0;   // invalid groups of the ring's steps, two bits each
+  int pv[2] = {0, 0};     // pages of the groups of steps (i & ~63) + lane
+  auto load_pages = [&](int i) {
+    const int n = i + lane;
+    const int p0 = n < mine ? units.unit(u0 + wave + n * kWaves) * kStep : 0;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) pv[g] = n < mine ? pages.page(a.c, p0 + g * 16) : -2;
+  };
+  auto issue = [&](int i, bool values) {
+    // past the end: loads that bring zeros, so that every wait counts the same
+    const int p0 = i < mine ? units.unit(u0 + wave + i * kWaves) * kStep : 0;
+    const uint32_t dst = ring + uint32_t((i & (NS - 1)) * 2 + (values ? 1 : 0)) * STEP;
+    constexpr int G = R::kLoads < 4 ? R::kLoads : 4;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int page = i < mine ? __builtin_amdgcn_readlane(pv[g], i & 63) : -2;
+      const uint32_t bit = 1u << (2 * (i & (NS - 1)) + g);
+      if (!values) ringbad = page == -1 ? ringbad | bit : ringbad & ~bit;
+      const i32x4 rs = group_rsrc(a.c, values ? a.c.v : a.c.k, page, p0 + g * 16, item.head, R::kBytes);
+#pragma unroll
+      for (int y = 0; y < R::kLoads / G; ++y) {
+        uint32_t off[G];
+#pragma unroll
+        for (int x = 0; x < G; ++x) {
+          const int r = (y * G + x) * R::kRowsPerLoad + lrow;
+          const int sw = values ? ValueReader16<T, F8, DIM>::swizzle(g * 16 + r) : R::key_swizzle(r);
+          off[x] = uint32_t(r) * uint32_t(a.c.token_stride) + uint32_t((lslot ^ sw) << 4);
+        }
+        dma16_group<G>(rs, off, dst + g * 16 * R::kBytes + y * 4096);
+      }
+    }
+  };
+  // queries: the second operand, lane's packed row col, 8 of its dimensions a product
+  load_pages(0);
+  int t[QT], low[QT];
+  x8 q[QT][KS];
+  const float sc = a.scale * kLog2e * (F8 ? a.c.k_scale[item.head] : 1.0f);
+  const uint32_t flip = sc < 0 ? 0x80008000u : 0u;                               // the scale's sign, exactly
+  const float c = __builtin_fmaxf(__builtin_fabsf(sc), 1.17549435e-38f);         // not 0: hidden scores are -inf
+#pragma unroll
+  for (int i = 0; i < QT; ++i) {
+    const int m = i * 16 + col, mc = min(m, M - 1);
+    const int j = mc / a.group, h = mc - j * a.group + item.head * a.group;
+    t[i] = m < M ? t0 + j : -1;
+    low[i] = a.window < 0 ? 0 : t[i] - a.window + 1;
+    const char* src = a.q + (sq.q_start + j) * a.q_row_stride + int64_t(h) * a.q_head_stride;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const int d = F8 ? (k >> 1) * 64 + qd * 16 + (k & 1) * 8 : k * 32 + qd * 8;
+      q[i][k] = __builtin_bit_cast(x8, *reinterpret_cast<const u32x4*>(src + d * 2) ^ flip);
+    }
+  }
+  // Queries and pages are in registers from here on, so every load in flight is the ring's.
+#pragma unroll
+  for (int i = 0; i < QT; ++i)
+#pragma unroll
+    for (int k = 0; k < KS; ++k) asm volatile("" : "+v"(q[i][k]));
+  asm volatile("s_waitcnt vmcnt(0)" : "+v"(pv[0]), "+v"(pv[1]) : : "memory");
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    issue(i, false);
+    issue(i, true);
+  }
+  f32x4 o[QT][DB];
+  float top[QT], sum[QT];
+#pragma unroll
+  for (int i = 0; i < QT; ++i) {
+    top[i] = kLowest;
+    sum[i] = 0;
+#pragma unroll
+    for (int d = 0; d < DB; ++d) o[i][d] = f32x4{0, 0, 0, 0};
+  }
+  const ValueReader16<T, F8, DIM> vr(lane);
+  const uint32_t kbase = uint32_t(col * R::kBytes + ((qd ^ R::key_swizzle(col)) << 4));
+  float* scores = nullptr;
+  if constexpr (MASS)
+    scores = a.scores + (int64_t(blockIdx.x) * a.score_rows + col) * part.score_cols + qd * 4;
+  bool again = false;
+
+  for (int i = 0; i < mine; ++i) {
+    const int p0 = units.unit(u0 + wave + i * kWaves) * kStep;
+    const uint32_t kt = ring + uint32_t((i & (NS - 1)) * 2) * STEP, vt = kt + STEP;
+    const uint32_t badp = (ringbad >> (2 * (i & (NS - 1)))) & 3u;
+    wait_vm<(2 * NS - 1) * NL>();   // all but what was issued after this step's keys
+    typedef __attribute__((address_space(3))) const u32x4* kp;
+    f32x4 st[QT][2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+#pragma unroll
+      for (int x = 0; x < QT; ++x) st[x][g] = f32x4{0, 0, 0, 0};
+      if constexpr (F8) {
+#pragma unroll
+        for (int k = 0; k < KS / 2; ++k) {
+          const u32x4 w = *kp(uintptr_t(kt + g * 16 * R::kBytes + (kbase ^ uint32_t(k * 64))));
+          const x8 k0 = from_e4m3<T>(w[0], w[1]), k1 = from_e4m3<T>(w[2], w[3]);
+#pragma unroll
+          for (int x = 0; x < QT; ++x) {
+            st[x][g] = mfma16<T>(k0, q[x][2 * k], st[x][g]);
+            st[x][g] = mfma16<T>(k1, q[x][2 * k + 1], st[x][g]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const x8 kf = __builtin_bit_cast(x8, *kp(uintptr_t(kt + g * 16 * R::kBytes + (kbase ^ uint32_t(k * 64)))));
+#pragma unroll
+          for (int x = 0; x < QT; ++x) st[x][g] = mfma16<T>(kf, q[x][k], st[x][g]);
+        }
+      }
+    }
+    if (((i + NS) & 63) == 0) load_pages(i + NS);
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");   // the keys are in registers: their place may be filled
+    issue(i + NS, false);
+
+    const bool masked = badp != 0 ||
+                        !(p0 + kStep - 1 <= t_lo && (a.window < 0 || p0 >= lowx || p0 + kStep - 1 < a.sinks));
+    if (masked) {
+#pragma unroll
+      for (int x = 0; x < QT; ++x)
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int p = p0 + g * 16 + qd * 4 + e;
+            const bool seen = p <= t[x] && (p >= low[x] || p < a.sinks);
+            const float v = (badp >> g) & 1u ? __builtin_nanf("") : st[x][g][e];
+            st[x][g][e] = seen ? v : -INFINITY;
+          }
+    }
+    x8 w[QT];
+#pragma unroll
+    for (int x = 0; x < QT; ++x) {
+      float mx = __builtin_fmaxf(st[x][0][0], st[x][1][0]);
+#pragma unroll
+      for (int e = 1; e < 4; ++e) mx = __builtin_fmaxf(mx, __builtin_fmaxf(st[x][0][e], st[x][1][e]));
+      mx = max_rows16(max_halves(mx)) * c;
+      if (__any(mx > top[x] + kLag)) {
+        const float next = __builtin_fmaxf(top[x], mx), keep = __builtin_amdgcn_exp2f(top[x] - next);
+        top[x] = next;
+        sum[x] *= keep;
+#pragma unroll
+        for (int d = 0; d < DB; ++d) o[x][d] *= keep;
+      }
+      u32x4 pk;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = st[x][g][e] * c;
+          const float wt = __builtin_amdgcn_exp2f(v[e] - top[x]);
+          sum[x] += wt;
+          st[x][g][e] = wt;
+        }
+        if constexpr (MASS) {
+          if (x * 16 + col < M)
+            *reinterpret_cast<f32x4*>(scores + int64_t(x) * 16 * part.score_cols + (wave + i * kWaves) * kStep + g * 16) = v;
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) pk[g * 2 + y] = pack_pair<T>(st[x][g][2 * y], st[x][g][2 * y + 1]);
+      }
+      w[x] = __builtin_bit_cast(x8, pk);
+    }
+    wait_vm<(2 * NS - 1) * NL>();
+    if (masked) {
+      // a hidden position may hold anything: infinities and NaN leave the values, and a row that sees one
+      // is gone over again
+      bool seen = false;
+      for (int at = lane * 16; at < STEP; at += 1024) {
+        typedef __attribute__((address_space(3))) u32x4* vp;
+        vp z = vp(uintptr_t(vt + at));
+        u32x4 f = *z;
+        if (!drop_nonfinite<T, F8>(f)) continue;
+        *z = f;
+        const int p = p0 + at / R::kBytes;
+        seen |= p <= t_hi && (p >= pages.lo_pos || p < a.sinks);
+      }
+      again |= __any(seen);
+      asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+    }
+#pragma unroll
+    for (int d = 0; d < DB; ++d) {
+      const x8 vf = __builtin_bit_cast(x8, vr.read(vt, d));
+#pragma unroll
+      for (int x = 0; x < QT; ++x) o[x][d] = mfma16<T>(vf, w[x], o[x][d]);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+    issue(i + NS, true);
+  }
+
+  wait_vm<0>();
+  if (__syncthreads_or(again)) {
+    for (int m = wave; m < M; m += kWaves)
+      slow_row<T, F8, DIM>(a, sq, pages, units, u0, nu, kStep, t0, item.head, m,
+                           sq.nsplit > 1 ? int64_t(blockIdx.x) * BM + m : -1,
+                           sq.nsplit > 1 || MASS ? int64_t(blockIdx.x) * BM + m : -1);
+    return;
+  }
+  // the waves' rows meet in LDS
+  float* mo = reinterpret_cast<float*>(lds + wave * WAVE_LDS);
+#pragma unroll
+  for (int x = 0; x < QT; ++x) {
+    if (x * 16 + col < M) {
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+        *reinterpret_cast<f32x4*>(mo + (x * 16 + col) * (DIM + 4) + d * 16 + qd * 4) = o[x][d];
+    }
+    float total = sum[x];
+    total += __shfl_xor(total, 16);
+    total += __shfl_xor(total, 32);
+    if (qd == 0) {
+      ml[wave][x * 16 + col][0] = top[x];
+      ml[wave][x * 16 + col][1] = total;
+    }
+  }
+  __syncthreads();
+  const float vs = F8 ? a.c.v_scale[item.head] : 1.0f;
+  for (int z = tid; z < M * (DIM / 4); z += kWaves * 64) {
+    const int m = z / (DIM / 4), d = (z - m * (DIM / 4)) * 4;
+    float best = ml[0][m][0];
+#pragma unroll
+    for (int y = 1; y < kWaves; ++y) best = __builtin_fmaxf(best, ml[y][m][0]);
+    float total = 0;
+    f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+    for (int y = 0; y < kWaves; ++y) {
+      const float f = __builtin_amdgcn_exp2f(ml[y][m][0] - best);
+      total += ml[y][m][1] * f;
+      acc += *reinterpret_cast<const f32x4*>(lds + y * WAVE_LDS + (m * (DIM + 4) + d) * 4) * f;
+    }
+    if (sq.nsplit > 1) {
+      const int64_t slot = int64_t(blockIdx.x) * BM + m;
+      *reinterpret_cast<f32x4*>(a.part_o + slot * DIM + d) = acc;
+      if (d == 0) *reinterpret_cast<f32x2*>(a.part_ml + slot * 2) = f32x2{best, total};
+    } else {
+      const float inv = total == 0 ? 0.0f : vs / total;
+      const int j = m / a.group;
+      const int64_t row = int64_t(sq.q_start + j) * a.heads + (m - j * a.group) + item.head * a.group;
+      *reinterpret_cast<u32x2*>(a.out + (row * DIM + d) * 2) =
+          u32x2{pack_pair<T>(acc[0] * inv, acc[1] * inv), pack_pair<T>(acc[2] * inv, acc[3] * inv)};
+      // accumulated weights are taken against these, also where the rows were not split
+      if (MASS && d == 0) *reinterpret_cast<f32x2*>(a.part_ml + (int64_t(blockIdx.x) * BM + m) * 2) = f32x2{best, total};
+    }
+  }
+}
+
+// ---------------------------------------------------------------- join
+//
+// One packed row a block: the item of split s takes the tile's rows s, s + nsplit, ... along blockIdx.y.
+// Four waves read a quarter of the splits' rows each.
+template <typename T, int DIM>
+__global__ __launch_bounds__(256) void join_kernel(AttnArgs a, AttnPart part, int tile_rows, bool f8) {
+  constexpr int PER = DIM / 64;
+  typedef float vec __attribute__((ext_vector_type(PER)));
+  __shared__ float acc[4][DIM];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int s = seq_of_item(part, blockIdx.x);
+  const AttnSeq sq = part.seq[s];
+  const int first = s == 0 ? 0 : part.seq[s - 1].item_end;
+  const int M = sq.rows * a.group, tiles = (M + tile_rows - 1) / tile_rows;
+  const AttnItem item = attn_item(int(blockIdx.x) - first, a.c.kv_heads, sq.nsplit, tiles);
+  const int r = item.split + sq.nsplit * int(blockIdx.y);
+  if (r >= tile_rows || r >= M - item.tile * tile_rows) return;
+  const int m = item.tile * tile_rows + r;
+  const int64_t slot0 = (int64_t(blockIdx.x) - item.split * a.c.kv_heads) * tile_rows + r;
+  const int64_t step = int64_t(a.c.kv_heads) * tile_rows;
+  float top = kLowest;
+  for (int i = lane; i < sq.nsplit; i += 64) top = __builtin_fmaxf(top, a.part_ml[(slot0 + i * step) * 2]);
+  for (int d = 1; d < 64; d <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
+  float total = 0;
+  for (int i = lane; i < sq.nsplit; i += 64) {
+    const f32x2 x = *reinterpret_cast<const f32x2*>(a.part_ml + (slot0 + i * step) * 2);
+    total += x[1] * exp2f(x[0] - top);
+  }
+  for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+  vec sum = {};
+#pragma unroll 4
+  for (int i = wave; i < sq.nsplit; i += 4) {
+    const int64_t slot = slot0 + i * step;
+    sum += *reinterpret_cast<const vec*>(a.part_o + slot * DIM + lane * PER) * exp2f(a.part_ml[slot * 2] - top);
+  }
+  *reinterpret_cast<vec*>(&acc[wave][lane * PER]) = sum;
+  __syncthreads();
+  const int j = m / a.group;
+  const int64_t row = int64_t(sq.q_start + j) * a.heads + (m - j * a.group) + item.head * a.group;
+  const float inv = total == 0 ? 0.0f : (f8 ? a.c.v_scale[item.head] : 1.0f) / total;
+  if (tid < DIM / 2) {
+    float x[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      x[e] = (acc[0][2 * tid + e] + acc[1][2 * tid + e] + acc[2][2 * tid + e] + acc[3][2 * tid + e]) * inv;
+    *reinterpret_cast<uint32_t*>(a.out + (row * DIM + 2 * tid) * 2) = pack_pair<T>(x[0], x[1]);
+  }
+  if (a.lse && tid == 0) a.lse[row] = total == 0 ? -INFINITY : top + __builtin_log2f(total);
+}
+
+template <typename T, bool F8, int DIM, int QT>
+void run_shape(const AttnArgs& a, const AttnPart& p, hipStream_t stream) {
+  const dim3 grid(p.items), block(kWaves * 64);
+  if (a.scores) hipLaunchKernelGGL((decode_kernel<T, F8, DIM, QT, true>), grid, block, 0, stream, a, p);
+  else hipLaunchKernelGGL((decode_kernel<T, F8, DIM, QT, false>), grid, block, 0, stream, a, p);
+}
+
+template <typename T, bool F8, int QT>
+void run_dim(const AttnArgs& a, const AttnPart& p, hipStream_t stream) {
+  if (a.c.dim == 256) run_shape<T, F8, 256, QT>(a, p, stream);
+  else if (a.c.dim == 128) run_shape<T, F8, 128, QT>(a, p, stream);
+  else run_shape<T, F8, 64, QT>(a, p, stream);
+}
+
+template <typename T, bool F8>
+void run_rows(const AttnArgs& a, const AttnPart& p, int rows, hipStream_t stream) {
+  if (rows <= 16) run_dim<T, F8, 1>(a, p, stream);
+  else run_dim<T, F8, 2>(a, p, stream);
+}
+
+// ---------------------------------------------------------------- accumulated weights of decoded rows
+//
+// A thread a position: the scores that the rows' items left in the workspace against the rows' totals.
+__global__ __launch_bounds__(256) void decode_mass_kernel(AttnArgs a, AttnPart part, int tile_rows) {
+  __shared__ float lse[kAttnDecodeMaxRows];
+  const int s = blockIdx.z, head = blockIdx.y;
+  const AttnSeq sq = part.seq[s];
+  const int first = s == 0 ? 0 : part.seq[s - 1].item_end;
+  if (int(blockIdx.x) * 256 >= sq.kv_len) return;
+  const int M = sq.rows * a.group;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int m = wave; m < M; m += 4) {
+    float top = kLowest, total = 0;
+    for (int i = lane; i < sq.nsplit; i += 64)
+      top = __builtin_fmaxf(top, a.part_ml[((int64_t(first) + i * a.c.kv_heads + head) * tile_rows + m) * 2]);
+    for (int d = 1; d < 64; d <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
+    for (int i = lane; i < sq.nsplit; i += 64) {
+      const f32x2 x = *reinterpret_cast<const f32x2*>(
+          a.part_ml + ((int64_t(first) + i * a.c.kv_heads + head) * tile_rows + m) * 2);
+      total += x[1] * exp2f(x[0] - top);
+    }
+    for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+    if (lane == 0) lse[m] = total == 0 ? INFINITY : top + __builtin_log2f(total);   // no position seen: no weight
+  }
+  __syncthreads();
+  const int p = blockIdx.x * 256 + threadIdx.x;
+  if (p >= sq.kv_len) return;
+  const int64_t at = (int64_t(sq.index) * a.c.kv_heads + head) * a.mass_cap + p;
+  float sum = 0;
+  const Units units = units_of(sq.kv_len - sq.rows, sq.kv_len - 1, a.window, a.sinks, kDecodeUnitShift);
+  const int unit = p >> kDecodeUnitShift;
+  const int u = unit < units.sinks ? unit : unit - units.gap;
+  if (unit < units.sinks || (u >= units.sinks && u < units.count)) {
+    const int split = int((int64_t(u + 1) * sq.nsplit - 1) / units.count);
+    const int b = first + split * a.c.kv_heads + head;
+    const float* sc = a.scores + int64_t(b) * a.score_rows * part.score_cols +
+                      (u - split_begin(units.count, split, sq.nsplit)) * kStep + (p & (kStep - 1));
+    for (int m = 0; m < M; ++m) {
+      const float x = sc[int64_t(m) * part.score_cols];
+      sum += x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(x - lse[m]);   // -inf: not seen
+    }
+  }
+  a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.0f) + sum;
+}
+
+}  // namespace
+
+hipError_t launch_attn_decode(const AttnArgs& a, const AttnPart& p, int rows, int dtype, int cache_dtype,
+                              hipStream_t stream) {
+  const bool f8 = cache_dtype == LORA_KV_E4M3;
+  if (dtype == LORA_KV_BF16) {
+    if (f8) run_rows<__bf16, true>(a, p, rows, stream);
+    else run_rows<__bf16, false>(a, p, rows, stream);
+  } else {
+    if (f8) run_rows<_Float16, true>(a, p, rows, stream);
+    else run_rows<_Float16, false>(a, p, rows, stream);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_attn_join(const AttnArgs& a, const AttnPart& p, int tile_rows, int most, int dtype,
+                            hipStream_t stream) {
+  const dim3 grid(p.split_items, most), block(256);
+  const bool f8 = a.c.v_scale != nullptr;
+  auto go = [&](auto* kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, p, tile_rows, f8); };
+  if (dtype == LORA_KV_BF16) {
+    if (a.c.dim == 256) go(join_kernel<__bf16, 256>);
+    else if (a.c.dim == 128) go(join_kernel<__bf16, 128>);
+    else go(join_kernel<__bf16, 64>);
+  } else {
+    if (a.c.dim == 256) go(join_kernel<_Float16, 256>);
+    else if (a.c.dim == 128) go(join_kernel<_Float16, 128>);
+    else go(join_kernel<_Float16, 64>);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_attn_mass_decode(const AttnArgs& a, const AttnPart& p, int tile_rows, hipStream_t stream) {
+  int longest = 0;
+  for (int i = 0; i < p.n; ++i) longest = p.seq[i].kv_len > longest ? p.seq[i].kv_len : longest;
+  if (longest == 0) return hipSuccess;
+  hipLaunchKernelGGL(decode_mass_kernel, dim3((longest + 255) / 256, a.c.kv_heads, p.n), dim3(256), 0, stream, a, p,
+                     tile_rows);
+  return hipGetLastError();
+}
+
+}  // namespace lora

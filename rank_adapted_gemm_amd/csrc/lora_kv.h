@@ -73,26 +73,101 @@ struct EvictArgs {
   int32_t budget, sinks, recent;
 };
 
+// ---------------------------------------------------------------- attention
+//
+// A sequence's rows and the query heads that share a key-value head are packed:
+// packed row m is row m / group, head m % group of the group, so all of them
+// meet the same keys and their positions never decrease.  The host cuts the
+// packed rows into tiles and the positions a tile sees into units, and splits a
+// tile's units over `nsplit` items where the tiles alone would leave CUs idle.
+
+constexpr int kAttnSeqs = 128;   // sequences of one launch: their table travels as a kernel argument
+
+struct AttnSeq {
+  int32_t q_start, rows, kv_len;
+  int32_t item_end;              // items of this and all earlier sequences
+  int32_t nsplit;
+  int32_t index;                 // the sequence's number in the batch
+};
+
+struct AttnPart {
+  int32_t n;
+  int32_t items, split_items;    // items of sequences with nsplit > 1 come first
+  int32_t score_cols;            // decode: positions of an item's score rows in the workspace
+  AttnSeq seq[kAttnSeqs];
+};
+
+// Positions seen by rows at t_lo .. t_hi, in units of 2^shift: unit(i) for i < count.
+struct Units {
+  int32_t sinks, gap, count;
+  __host__ __device__ int unit(int i) const { return i < sinks ? i : i + gap; }
+};
+
+__host__ __device__ inline Units units_of(int t_lo, int t_hi, int window, int sinks, int shift) {
+  Units u{0, 0, (t_hi >> shift) + 1};
+  if (window < 0) return u;
+  const int lo = t_lo - window + 1 > 0 ? t_lo - window + 1 : 0;
+  const int first = lo > t_hi || window == 0 ? u.count : lo >> shift;
+  const int seen = sinks < t_hi + 1 ? sinks : t_hi + 1;
+  const int ns = (seen + (1 << shift) - 1) >> shift;
+  if (ns >= first) return u;
+  u.sinks = ns;
+  u.gap = first - ns;
+  u.count -= u.gap;
+  return u;
+}
+
+// An item's place: its sequence, key-value head, tile of packed rows and split.
+struct AttnItem {
+  int32_t head, split, tile;
+};
+
+__host__ __device__ inline AttnItem attn_item(int r, int kv_heads, int nsplit, int tiles) {
+  const int per = r / kv_heads, back = per / nsplit;
+  return AttnItem{r - per * kv_heads, per - back * nsplit, tiles - 1 - back};   // the tiles that see most come first
+}
+
+// First unit (by number) of split s out of n over `count` units.
+__host__ __device__ inline int split_begin(int count, int s, int n) { return int(int64_t(count) * s / n); }
+
 struct AttnArgs {
   KvView c;
-  KvSeqs s;
+  const int32_t* table;
+  int64_t table_stride;
   const char* q;
   char* out;
   const float* mass_in;
   float* mass_out;
-  float* lse;            // workspace: per (row, head), base 2
+  float* lse;            // workspace: per (row, head), base 2 (prompts with accumulated weights), or NULL
+  float* part_o;         // workspace: unnormalised output rows of split items
+  float* part_ml;        // workspace: their maximum and sum
+  float* scores;         // workspace: scaled scores of decode items (accumulated weights), or NULL
   int64_t q_row_stride;  // bytes
   int64_t mass_cap;
   int32_t q_head_stride; // bytes
   int32_t heads, group;  // query heads; query heads per key-value head
-  int32_t rows, max_len;
+  int32_t score_rows;    // rows of a decode item's score block
   int32_t window, sinks;
   float scale;
 };
 
+// Shapes of the two attention kernels.
+constexpr int kDecodeUnitShift = 5;   // 32 positions, one wave's step
+constexpr int kPromptUnitShift = 6;   // 64 positions, one block's step
+constexpr int kAttnDecodeRows = 16;       // packed rows a decode tile holds for each 16-row column of the product
+constexpr int kAttnDecodeMaxRows = 32;    // sequences of at most that many packed rows are decoded
+constexpr int kPromptRows = 256;      // packed rows of a prompt tile
+constexpr int kMassRows = 128;        // positions of a prompt's weight block
+
 hipError_t launch_kv_append(const AppendArgs& a, int dtype, int cache_dtype, hipStream_t stream);
 hipError_t launch_kv_evict(const EvictArgs& a, int cache_dtype, hipStream_t stream);
-hipError_t launch_attn(const AttnArgs& a, int dtype, int cache_dtype, hipStream_t stream);
-hipError_t launch_attn_mass(const AttnArgs& a, int dtype, int cache_dtype, hipStream_t stream);
+hipError_t launch_attn_prompt(const AttnArgs& a, const AttnPart& p, int dtype, int cache_dtype, hipStream_t stream);
+hipError_t launch_attn_decode(const AttnArgs& a, const AttnPart& p, int rows, int dtype, int cache_dtype,
+                              hipStream_t stream);
+hipError_t launch_attn_join(const AttnArgs& a, const AttnPart& p, int tile_rows, int most, int dtype,
+                            hipStream_t stream);
+hipError_t launch_attn_mass_prompt(const AttnArgs& a, const AttnPart& p, int dtype, int cache_dtype,
+                                   hipStream_t stream);
+hipError_t launch_attn_mass_decode(const AttnArgs& a, const AttnPart& p, int tile_rows, hipStream_t stream);
 
 }  // namespace lora

@@ -3,6 +3,7 @@
 
 #include <algorithm>
 
+#include "lora_attn_plan.h"
 #include "lora_kv.h"
 
 namespace {
@@ -101,10 +102,6 @@ bool hits_cache(const void* p, size_t n, const KvView& c, size_t pool_bytes) {
   return overlaps(p, n, c.k, pool_bytes) || overlaps(p, n, c.v, pool_bytes);
 }
 
-size_t attn_need(const KvSeqs& s, int32_t n_heads, bool with_mass) {
-  return with_mass ? size_t(s.q_start[s.n]) * size_t(n_heads) * 4 : 0;
-}
-
 lora_status check_heads(const KvView& c, const KvSeqs& s, int32_t n_heads) {
   if (n_heads < 1 || n_heads % c.kv_heads != 0) return LORA_EINVAL;
   if (n_heads > 512) return LORA_EUNSUPPORTED;
@@ -148,7 +145,10 @@ size_t lora_attn_workspace_bytes(const lora_kv_cache* cache, const lora_kv_batch
   if (check_cache(cache, c, pool) != LORA_OK || check_batch(batch, cache->page_size, true, s) != LORA_OK ||
       check_heads(c, s, n_heads) != LORA_OK || sinks < 0)
     return 0;
-  return attn_need(s, n_heads, with_mass != 0);
+  if (s.n == 0 || (s.q_start[s.n] == 0 && !with_mass)) return 0;
+  lora::AttnPlan plan;
+  lora::attn_plan(plan, c, s, n_heads, window, sinks, with_mass != 0, int(elem_bytes(cache->dtype)));
+  return plan.bytes;
 }
 
 lora_status lora_attn(const lora_kv_cache* cache, const lora_kv_batch* batch,
@@ -157,36 +157,39 @@ lora_status lora_attn(const lora_kv_cache* cache, const lora_kv_batch* batch,
                       void* out, const float* mass_in, float* mass_out, int64_t mass_cap,
                       void* workspace, size_t workspace_bytes, hipStream_t stream) {
   lora::AttnArgs a;
+  KvSeqs seqs;
   size_t pool = 0;
   lora_status st = check_cache(cache, a.c, pool);
   if (st != LORA_OK) return st;
-  if ((st = check_batch(batch, cache->page_size, true, a.s)) != LORA_OK) return st;
-  if ((st = check_heads(a.c, a.s, n_heads)) != LORA_OK) return st;
+  if ((st = check_batch(batch, cache->page_size, true, seqs)) != LORA_OK) return st;
+  if ((st = check_heads(a.c, seqs, n_heads)) != LORA_OK) return st;
   if (!row_dtype_ok(dtype)) return LORA_EUNSUPPORTED;
   if (cache->dtype != LORA_KV_E4M3 && cache->dtype != int(dtype)) return LORA_EINVAL;
   if (sinks < 0) return LORA_EINVAL;
   if (mass_in && !mass_out) return LORA_EINVAL;
-  a.rows = a.s.n ? a.s.q_start[a.s.n] : 0;
-  a.max_len = 0;
-  for (int i = 0; i < a.s.n; ++i) a.max_len = std::max(a.max_len, a.s.kv_len[i]);
-  if (a.rows == 0 && (!mass_out || a.max_len == 0)) return LORA_OK;
+  const int rows = seqs.n ? seqs.q_start[seqs.n] : 0;
+  int longest = 0;
+  for (int i = 0; i < seqs.n; ++i) longest = std::max(longest, seqs.kv_len[i]);
+  if (rows == 0 && (!mass_out || longest == 0)) return LORA_OK;
 
   size_t q_span = 0, out_bytes = 0;
-  if (a.rows > 0) {
+  if (rows > 0) {
     if (!stride_ok(q_row_stride, a.c.dim, 2) || !stride_ok(q_head_stride, a.c.dim, 2)) return LORA_EINVAL;
     if (q_head_stride >= (int64_t(1) << 20)) return LORA_EUNSUPPORTED;
     if (!q || !out || !aligned16(q) || !aligned16(out)) return LORA_EINVAL;
-    q_span = span_bytes(a.rows, q_row_stride, n_heads, q_head_stride, a.c.dim, 2);
-    out_bytes = size_t(a.rows) * size_t(n_heads) * size_t(a.c.dim) * 2;
+    q_span = span_bytes(rows, q_row_stride, n_heads, q_head_stride, a.c.dim, 2);
+    out_bytes = size_t(rows) * size_t(n_heads) * size_t(a.c.dim) * 2;
   }
   size_t mass_bytes = 0;
   if (mass_out) {
-    if (mass_cap < a.max_len || mass_cap > (int64_t(1) << 32)) return LORA_EINVAL;
+    if (mass_cap < longest || mass_cap > (int64_t(1) << 32)) return LORA_EINVAL;
     if (!aligned4(mass_out) || !aligned4(mass_in)) return LORA_EINVAL;
-    mass_bytes = size_t(a.s.n) * size_t(a.c.kv_heads) * size_t(mass_cap) * 4;
+    mass_bytes = size_t(seqs.n) * size_t(a.c.kv_heads) * size_t(mass_cap) * 4;
     if (mass_in && mass_in != mass_out && overlaps(mass_in, mass_bytes, mass_out, mass_bytes)) return LORA_EINVAL;
   }
-  const size_t need = attn_need(a.s, n_heads, mass_out != nullptr);
+  lora::AttnPlan plan;
+  lora::attn_plan(plan, a.c, seqs, n_heads, window, sinks, mass_out != nullptr, int(elem_bytes(cache->dtype)));
+  const size_t need = plan.bytes;
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return LORA_EWORKSPACE;
     if (!aligned16(workspace)) return LORA_EINVAL;
@@ -209,18 +212,42 @@ lora_status lora_attn(const lora_kv_cache* cache, const lora_kv_batch* batch,
   a.out = static_cast<char*>(out);
   a.mass_in = mass_in;
   a.mass_out = mass_out;
-  a.lse = mass_out ? static_cast<float*>(workspace) : nullptr;
+  char* ws = static_cast<char*>(workspace);
+  a.table = batch->page_table;
+  a.table_stride = batch->table_stride;
+  a.lse = nullptr;
+  a.part_ml = reinterpret_cast<float*>(ws + plan.off_ml);
+  a.part_o = reinterpret_cast<float*>(ws + plan.off_o);
+  a.scores = mass_out ? reinterpret_cast<float*>(ws + plan.off_scores) : nullptr;
   a.q_row_stride = q_row_stride * 2;
   a.q_head_stride = int32_t(q_head_stride * 2);
   a.mass_cap = mass_cap;
   a.heads = n_heads;
   a.group = n_heads / a.c.kv_heads;
+  a.score_rows = plan.decode_rows;
   a.window = window;
   a.sinks = sinks;
   a.scale = scale;
+  // Launches of one call follow each other on the stream and share the workspace's sums.
   hipError_t e = hipSuccess;
-  if (a.rows > 0) e = lora::launch_attn(a, dtype, cache->dtype, stream);
-  if (e == hipSuccess && mass_out) e = lora::launch_attn_mass(a, dtype, cache->dtype, stream);
+  for (int i = 0; i < plan.decode.parts && e == hipSuccess; ++i) {
+    const lora::AttnPart& p = plan.decode.part[i];
+    if (p.items > 0) e = lora::launch_attn_decode(a, p, plan.decode_rows, dtype, cache->dtype, stream);
+    if (e == hipSuccess && p.split_items > 0)
+      e = lora::launch_attn_join(a, p, plan.decode_tile, plan.decode.join_rows[i], dtype, stream);
+    if (e == hipSuccess && mass_out) e = lora::launch_attn_mass_decode(a, p, plan.decode_tile, stream);
+  }
+  a.lse = mass_out ? reinterpret_cast<float*>(ws + plan.off_lse) : nullptr;
+  for (int i = 0; i < plan.prompt.parts && e == hipSuccess; ++i) {
+    lora::AttnPart& p = plan.prompt.part[i];
+    e = lora::launch_attn_prompt(a, p, dtype, cache->dtype, stream);
+    if (e == hipSuccess && p.split_items > 0)
+      e = lora::launch_attn_join(a, p, lora::kPromptRows, plan.prompt.join_rows[i], dtype, stream);
+    if (e == hipSuccess && mass_out) {
+      lora::attn_mass_part(p, a.c.kv_heads);
+      e = lora::launch_attn_mass_prompt(a, p, dtype, cache->dtype, stream);
+    }
+  }
   return e == hipSuccess ? LORA_OK : LORA_EHIP;
 }
 
