@@ -22,16 +22,12 @@ KV_DTYPES = {"bf16": 0, "f16": 1, "e4m3": 2}
 MAX_KV_LEN, MAX_PAGE_SIZE, MAX_HEADS = 1 << 24, 65536, 512
 
 
-def _row_dtypes():
-    import torch
-    return {torch.bfloat16: 0, torch.float16: 1}
-
-
 def _strides3(name, t, dim):
     """Element strides of a (rows, heads, dim) tensor; a dimension of one element has no stride of its own."""
-    if t.dim() != 3 or t.shape[2] != dim or t.stride(2) != 1:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != dim or stride[2] != 1:
         raise ValueError(f"{name} must be (rows, heads, {dim}) with a contiguous last dimension")
-    return [t.stride(i) if t.shape[i] > 1 else max(dim, 8) for i in range(2)]
+    return stride[0] if shape[0] > 1 else max(dim, 8), stride[1] if shape[1] > 1 else max(dim, 8)
 
 
 class KVCache:
@@ -63,6 +59,9 @@ class KVCache:
                                     v_scale.data_ptr() if v_scale is not None else None, self.n_pages, page, token,
                                     head, self.page_size, self.kv_heads, self.head_dim, KV_DTYPES[self.dtype])
         self._ref = ctypes.byref(self._c)
+        self._index = k.get_device()
+        # the types of new rows and queries that go with the cache, and their codes
+        self._row_codes = {torch.bfloat16: 0, torch.float16: 1} if self.dtype == "e4m3" else {k.dtype: KV_DTYPES[self.dtype]}
 
 
 class KVBatch:
@@ -80,6 +79,7 @@ class KVBatch:
         self.n_seq, self.rows = n, int(q_starts[-1])
         self.kv_len = [int(x) for x in kv_len]
         self.max_len = max(self.kv_len, default=0)
+        self._pages, self._index = page_table.shape[1], page_table.get_device()
         self._starts = (ctypes.c_int32 * (n + 1))(*[int(x) for x in q_starts])
         self._lens = (ctypes.c_int32 * max(n, 1))(*self.kv_len)
         self._c = _bd.KVBatchStruct(ctypes.cast(self._starts, ctypes.c_void_p),
@@ -95,33 +95,44 @@ def _table(name, t, n, torch):
     return t, (t.stride(0) if n > 1 else t.shape[1])
 
 
-def _pages_fit(cache, batch, lens, table, name):
+def _pages_fit(cache, pages, most, name):
     """Every sequence's pages lie inside its row of the table (the library sees the row stride alone)."""
-    most = max(lens, default=0)
-    if table.shape[1] * cache.page_size < most:
-        raise ValueError(f"{name} holds {table.shape[1]} pages of {cache.page_size} a sequence, {most} positions "
-                         "need more")
+    if pages * cache.page_size < most:
+        raise ValueError(f"{name} holds {pages} pages of {cache.page_size} a sequence, {most} positions need more")
 
 
-def _check_rows(cache, batch, named):
-    import torch
-    if batch.device != cache.device:
+def _check_batch(cache, batch):
+    if batch._index != cache._index:
         raise ValueError(f"the batch's page table is on {batch.device}, the cache on {cache.device}")
-    _pages_fit(cache, batch, batch.kv_len, batch.page_table, "page_table")
-    want = None if cache.dtype == "e4m3" else cache.k.dtype
-    for name, t in named.items():
-        if not t.is_cuda or t.device != cache.device:
-            raise ValueError(f"{name} must be a CUDA tensor on {cache.device}")
-        if t.dtype not in (torch.bfloat16, torch.float16) or (want is not None and t.dtype != want):
-            raise ValueError(f"{name} must be {want or 'bfloat16 or float16'}")
-        if t.shape[0] != batch.rows:
-            raise ValueError(f"{name} has {t.shape[0]} rows, the batch {batch.rows}")
+    _pages_fit(cache, batch._pages, batch.max_len, "page_table")
 
 
-def _mass_ptr(name, t, shape, dev, torch):
+def _row_code(cache, batch, name, t):
+    """The library's code of t's type, t being rows of the batch on the cache's device."""
+    if t.get_device() != cache._index:
+        raise ValueError(f"{name} must be a CUDA tensor on {cache.device}")
+    code = cache._row_codes.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be one of {list(cache._row_codes)}")
+    if t.shape[0] != batch.rows:
+        raise ValueError(f"{name} has {t.shape[0]} rows, the batch {batch.rows}")
+    return code
+
+
+def _empty(shape, dtype, dev, stream):
+    """A new tensor, allocated for the stream that writes it."""
+    import torch
+    if stream is None:   # torch's current one
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _mass_ptr(name, t, shape, dev):
+    import torch
     if t is None:
         return None
-    if t.dtype != torch.float32 or not t.is_cuda or t.device != dev or not t.is_contiguous() or tuple(t.shape) != shape:
+    if t.dtype != torch.float32 or t.device != dev or not t.is_contiguous() or tuple(t.shape) != shape:
         raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape} on {dev}")
     return t.data_ptr()
 
@@ -134,14 +145,15 @@ def _raise(status):
 def kv_append(cache, batch, k, v, stream=None):
     """Store the batch's new rows k, v (rows, kv_heads, head_dim; equal strides) at the last positions of
     their sequences, rounded to e4m3 codes of x / scale when the cache holds those."""
-    _check_rows(cache, batch, {"k": k, "v": v})
+    _check_batch(cache, batch)
+    code = _row_code(cache, batch, "k", k)
     strides = _strides3("k", k, cache.head_dim)
-    if k.dtype != v.dtype or k.shape != v.shape or k.shape[1] != cache.kv_heads or \
+    if code != _row_code(cache, batch, "v", v) or k.shape != v.shape or k.shape[1] != cache.kv_heads or \
             strides != _strides3("v", v, cache.head_dim):
         raise ValueError("k and v must be (rows, kv_heads, head_dim) of one type and the same strides")
     s = _bd._stream_of(stream, cache.device)
     _raise(_bd.load().lora_kv_append(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), strides[0], strides[1],
-                                     _row_dtypes()[k.dtype], s.cuda_stream))
+                                     code, s.cuda_stream))
 
 
 def attn_workspace_bytes(cache, batch, heads, window=-1, sinks=0, mass=False):
@@ -157,8 +169,8 @@ def attn_workspace(cache, batch, heads, window=-1, sinks=0, mass=False, stream=N
     need = attn_workspace_bytes(cache, batch, heads, window, sinks, mass)
     if not need:
         return None
-    with torch.cuda.stream(_bd._stream_of(stream, cache.device)):
-        return torch.empty(need, dtype=torch.uint8, device=cache.device)
+    _bd._stream_of(stream, cache.device)
+    return _empty(need, torch.uint8, cache.device, stream)
 
 
 def attn(cache, batch, q, scale=None, window=-1, sinks=0, out=None, mass=None, mass_out=None, workspace=None,
@@ -169,34 +181,32 @@ def attn(cache, batch, q, scale=None, window=-1, sinks=0, out=None, mass=None, m
     ``scale`` defaults to head_dim ** -0.5.  ``window`` >= 0 limits a row to that many positions up to its
     own, ``sinks`` first positions stay visible.  ``mass_out`` (n_seq, kv_heads, cap) float32 receives
     ``mass`` (zeros without it; it may be mass_out itself) plus the weight each position got."""
-    import torch
-    _check_rows(cache, batch, {"q": q})
+    _check_batch(cache, batch)
+    code = _row_code(cache, batch, "q", q)
     strides = _strides3("q", q, cache.head_dim)
     heads = q.shape[1]
     dev = cache.device
     s = _bd._stream_of(stream, dev)
     if out is None:
-        with torch.cuda.stream(s):
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        out = _empty(q.shape, q.dtype, dev, stream)
     elif out.dtype != q.dtype or out.device != dev or not out.is_contiguous() or out.shape != q.shape:
         raise ValueError("out must be a contiguous tensor like q")
-    cap = 0
-    if mass_out is not None:
-        cap = mass_out.shape[-1]
+    cap, m_in, m_out = 0, None, None
+    if mass_out is not None or mass is not None:
+        cap = (mass if mass_out is None else mass_out).shape[-1]
         if cap < batch.max_len:
             raise ValueError(f"mass_out holds {cap} positions, the batch reaches {batch.max_len}")
-    shape = (batch.n_seq, cache.kv_heads, cap)
-    m_in, m_out = _mass_ptr("mass", mass, shape, dev, torch), _mass_ptr("mass_out", mass_out, shape, dev, torch)
+        shape = (batch.n_seq, cache.kv_heads, cap)
+        m_in, m_out = _mass_ptr("mass", mass, shape, dev), _mass_ptr("mass_out", mass_out, shape, dev)
     if workspace is None:
-        workspace = attn_workspace(cache, batch, heads, window, sinks, mass_out is not None, s)
-    elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+        workspace = attn_workspace(cache, batch, heads, window, sinks, mass_out is not None, stream)
+    elif workspace.get_device() != cache._index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous CUDA tensor on {dev}")
     ws, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None \
         else (None, 0)
-    _raise(_bd.load().lora_attn(cache._ref, batch._ref, q.data_ptr(), strides[0], strides[1], heads,
-                                _row_dtypes()[q.dtype], cache.head_dim ** -0.5 if scale is None else float(scale),
-                                int(window), int(sinks), out.data_ptr(), m_in, m_out, cap, ws, ws_bytes,
-                                s.cuda_stream))
+    _raise(_bd.load().lora_attn(cache._ref, batch._ref, q.data_ptr(), strides[0], strides[1], heads, code,
+                                cache.head_dim ** -0.5 if scale is None else float(scale), int(window), int(sinks),
+                                out.data_ptr(), m_in, m_out, cap, ws, ws_bytes, s.cuda_stream))
     return out
 
 
@@ -209,28 +219,25 @@ def kv_evict(cache, batch, mass, budget, dst_table, sinks=0, recent=0, kept=None
     min(kv_len[i], budget)."""
     import torch
     dev = cache.device
-    if batch.device != dev:
-        raise ValueError(f"the batch's page table is on {batch.device}, the cache on {dev}")
-    _pages_fit(cache, batch, batch.kv_len, batch.page_table, "page_table")
+    _check_batch(cache, batch)
     budget = int(budget)
     dst_table, dst_stride = _table("dst_table", dst_table, batch.n_seq, torch)
-    if dst_table.device != dev:
+    if dst_table.get_device() != cache._index:
         raise ValueError(f"dst_table must be on {dev}")
-    _pages_fit(cache, batch, [min(n, budget) for n in batch.kv_len], dst_table, "dst_table")
+    _pages_fit(cache, dst_table.shape[1], min(batch.max_len, budget), "dst_table")
     cap = mass.shape[-1]
     if cap < batch.max_len:
         raise ValueError(f"mass holds {cap} positions, the batch reaches {batch.max_len}")
-    m_in = _mass_ptr("mass", mass, (batch.n_seq, cache.kv_heads, cap), dev, torch)
+    m_in = _mass_ptr("mass", mass, (batch.n_seq, cache.kv_heads, cap), dev)
     shape = (batch.n_seq, cache.kv_heads, max(budget, 0))
     s = _bd._stream_of(stream, dev)
-    with torch.cuda.stream(s):
-        if kept is None:
-            kept = torch.empty(shape, dtype=torch.int32, device=dev)
-        if mass_out is None:
-            mass_out = torch.empty(shape, dtype=torch.float32, device=dev)
-    if kept.dtype != torch.int32 or kept.device != dev or not kept.is_contiguous() or tuple(kept.shape) != shape:
+    if kept is None:
+        kept = _empty(shape, torch.int32, dev, stream)
+    elif kept.dtype != torch.int32 or kept.device != dev or not kept.is_contiguous() or tuple(kept.shape) != shape:
         raise ValueError(f"kept must be a contiguous int32 tensor of shape {shape} on {dev}")
-    m_out = _mass_ptr("mass_out", mass_out, shape, dev, torch)
+    if mass_out is None:
+        mass_out = _empty(shape, torch.float32, dev, stream)
+    m_out = _mass_ptr("mass_out", mass_out, shape, dev)
     _raise(_bd.load().lora_kv_evict(cache._ref, batch._ref, m_in, cap, budget, int(sinks), int(recent),
                                     dst_table.data_ptr(), dst_stride, kept.data_ptr(), m_out, s.cuda_stream))
     return kept, mass_out

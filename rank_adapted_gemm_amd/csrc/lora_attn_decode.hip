@@ -340,52 +340,108 @@ __global__ __launch_bounds__(kWaves * 64, 1) void decode_kernel(AttnArgs a, Attn
 
 // ---------------------------------------------------------------- join
 //
-// One packed row a block: the item of split s takes the tile's rows s, s + nsplit, ... along blockIdx.y.
-// Four waves read a quarter of the splits' rows each.
+// Bound by the sums it reads.  The item of split s takes the tile's rows s, s + nsplit, ..., so that all
+// items of a tile share the work.  Few splits: a wave a row, all of its loads under way at once.
+constexpr int kJoinFew = 8;
+
+struct JoinRow {
+  int64_t slot, step;   // the row's place in the first split's sums; from one split to the next
+  int64_t row;          // (row, head) of the output
+  int nsplit, head;
+  bool valid;
+};
+
+__device__ __forceinline__ JoinRow join_row(const AttnArgs& a, const AttnPart& part, int tile_rows, int nth) {
+  const int s = seq_of_item(part, blockIdx.x);
+  const AttnSeq sq = part.seq[s];
+  const int first = s == 0 ? 0 : part.seq[s - 1].item_end;
+  const int M = sq.rows * a.group, tiles = (M - 1) / tile_rows + 1;
+  const AttnItem item = attn_item(int(blockIdx.x) - first, a.c.kv_heads, sq.nsplit, tiles);
+  const int r = item.split + sq.nsplit * nth, m = item.tile * tile_rows + r;
+  JoinRow o;
+  o.valid = r < tile_rows && r < M - item.tile * tile_rows;
+  o.slot = (int64_t(blockIdx.x) - item.split * a.c.kv_heads) * tile_rows + r;
+  o.step = int64_t(a.c.kv_heads) * tile_rows;
+  const int j = m / a.group;
+  o.row = int64_t(sq.q_start + j) * a.heads + (m - j * a.group) + item.head * a.group;
+  o.nsplit = sq.nsplit;
+  o.head = item.head;
+  return o;
+}
+
+template <typename T, int DIM>
+__global__ __launch_bounds__(256) void join_few_kernel(AttnArgs a, AttnPart part, int tile_rows, bool f8) {
+  constexpr int PER = DIM / 64;
+  typedef float vec __attribute__((ext_vector_type(PER)));
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const JoinRow x = join_row(a, part, tile_rows, int(blockIdx.y) * 4 + wave);
+  if (!x.valid) return;
+  vec o[kJoinFew];
+  f32x2 ml[kJoinFew];
+#pragma unroll
+  for (int i = 0; i < kJoinFew; ++i) {
+    const int64_t slot = x.slot + (i < x.nsplit ? i : 0) * x.step;   // past the end: the first again
+    ml[i] = *reinterpret_cast<const f32x2*>(a.part_ml + slot * 2);
+    o[i] = *reinterpret_cast<const vec*>(a.part_o + slot * DIM + lane * PER);
+  }
+  float top = ml[0][0];
+#pragma unroll
+  for (int i = 1; i < kJoinFew; ++i) top = __builtin_fmaxf(top, ml[i][0]);
+  float total = 0;
+  vec sum = {};
+#pragma unroll
+  for (int i = 0; i < kJoinFew; ++i) {
+    if (i >= x.nsplit) continue;
+    const float f = exp2f(ml[i][0] - top);
+    total += ml[i][1] * f;
+    sum += o[i] * f;
+  }
+  const float inv = total == 0 ? 0.0f : (f8 ? a.c.v_scale[x.head] : 1.0f) / total;
+  T* dst = reinterpret_cast<T*>(a.out) + x.row * DIM + lane * PER;
+  if constexpr (PER == 4)
+    *reinterpret_cast<u32x2*>(dst) = u32x2{pack_pair<T>(sum[0] * inv, sum[1] * inv), pack_pair<T>(sum[2] * inv, sum[3] * inv)};
+  else if constexpr (PER == 2)
+    *reinterpret_cast<uint32_t*>(dst) = pack_pair<T>(sum[0] * inv, sum[1] * inv);
+  else
+    *dst = T(sum[0] * inv);
+  if (a.lse && lane == 0) a.lse[x.row] = total == 0 ? -INFINITY : top + __builtin_log2f(total);
+}
+
+// Many splits: a block a row, each of its four waves a quarter of the splits.
 template <typename T, int DIM>
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, AttnPart part, int tile_rows, bool f8) {
   constexpr int PER = DIM / 64;
   typedef float vec __attribute__((ext_vector_type(PER)));
   __shared__ float acc[4][DIM];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int s = seq_of_item(part, blockIdx.x);
-  const AttnSeq sq = part.seq[s];
-  const int first = s == 0 ? 0 : part.seq[s - 1].item_end;
-  const int M = sq.rows * a.group, tiles = (M + tile_rows - 1) / tile_rows;
-  const AttnItem item = attn_item(int(blockIdx.x) - first, a.c.kv_heads, sq.nsplit, tiles);
-  const int r = item.split + sq.nsplit * int(blockIdx.y);
-  if (r >= tile_rows || r >= M - item.tile * tile_rows) return;
-  const int m = item.tile * tile_rows + r;
-  const int64_t slot0 = (int64_t(blockIdx.x) - item.split * a.c.kv_heads) * tile_rows + r;
-  const int64_t step = int64_t(a.c.kv_heads) * tile_rows;
+  const JoinRow r = join_row(a, part, tile_rows, blockIdx.y);
+  if (!r.valid) return;
   float top = kLowest;
-  for (int i = lane; i < sq.nsplit; i += 64) top = __builtin_fmaxf(top, a.part_ml[(slot0 + i * step) * 2]);
+  for (int i = lane; i < r.nsplit; i += 64) top = __builtin_fmaxf(top, a.part_ml[(r.slot + i * r.step) * 2]);
   for (int d = 1; d < 64; d <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
   float total = 0;
-  for (int i = lane; i < sq.nsplit; i += 64) {
-    const f32x2 x = *reinterpret_cast<const f32x2*>(a.part_ml + (slot0 + i * step) * 2);
+  for (int i = lane; i < r.nsplit; i += 64) {
+    const f32x2 x = *reinterpret_cast<const f32x2*>(a.part_ml + (r.slot + i * r.step) * 2);
     total += x[1] * exp2f(x[0] - top);
   }
   for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
   vec sum = {};
 #pragma unroll 4
-  for (int i = wave; i < sq.nsplit; i += 4) {
-    const int64_t slot = slot0 + i * step;
+  for (int i = wave; i < r.nsplit; i += 4) {
+    const int64_t slot = r.slot + i * r.step;
     sum += *reinterpret_cast<const vec*>(a.part_o + slot * DIM + lane * PER) * exp2f(a.part_ml[slot * 2] - top);
   }
   *reinterpret_cast<vec*>(&acc[wave][lane * PER]) = sum;
   __syncthreads();
-  const int j = m / a.group;
-  const int64_t row = int64_t(sq.q_start + j) * a.heads + (m - j * a.group) + item.head * a.group;
-  const float inv = total == 0 ? 0.0f : (f8 ? a.c.v_scale[item.head] : 1.0f) / total;
+  const float inv = total == 0 ? 0.0f : (f8 ? a.c.v_scale[r.head] : 1.0f) / total;
   if (tid < DIM / 2) {
     float x[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       x[e] = (acc[0][2 * tid + e] + acc[1][2 * tid + e] + acc[2][2 * tid + e] + acc[3][2 * tid + e]) * inv;
-    *reinterpret_cast<uint32_t*>(a.out + (row * DIM + 2 * tid) * 2) = pack_pair<T>(x[0], x[1]);
+    *reinterpret_cast<uint32_t*>(a.out + (r.row * DIM + 2 * tid) * 2) = pack_pair<T>(x[0], x[1]);
   }
-  if (a.lse && tid == 0) a.lse[row] = total == 0 ? -INFINITY : top + __builtin_log2f(total);
+  if (a.lse && tid == 0) a.lse[r.row] = total == 0 ? -INFINITY : top + __builtin_log2f(total);
 }
 
 template <typename T, bool F8, int DIM, int QT>
@@ -470,17 +526,20 @@ hipError_t launch_attn_decode(const AttnArgs& a, const AttnPart& p, int rows, in
 
 hipError_t launch_attn_join(const AttnArgs& a, const AttnPart& p, int tile_rows, int most, int dtype,
                             hipStream_t stream) {
-  const dim3 grid(p.split_items, most), block(256);
+  int splits = 0;
+  for (int i = 0; i < p.n; ++i) splits = p.seq[i].nsplit > splits ? p.seq[i].nsplit : splits;
+  const bool few = splits <= kJoinFew;
+  const dim3 grid(p.split_items, few ? (most + 3) / 4 : most), block(256);
   const bool f8 = a.c.v_scale != nullptr;
   auto go = [&](auto* kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, p, tile_rows, f8); };
   if (dtype == LORA_KV_BF16) {
-    if (a.c.dim == 256) go(join_kernel<__bf16, 256>);
-    else if (a.c.dim == 128) go(join_kernel<__bf16, 128>);
-    else go(join_kernel<__bf16, 64>);
+    if (a.c.dim == 256) go(few ? join_few_kernel<__bf16, 256> : join_kernel<__bf16, 256>);
+    else if (a.c.dim == 128) go(few ? join_few_kernel<__bf16, 128> : join_kernel<__bf16, 128>);
+    else go(few ? join_few_kernel<__bf16, 64> : join_kernel<__bf16, 64>);
   } else {
-    if (a.c.dim == 256) go(join_kernel<_Float16, 256>);
-    else if (a.c.dim == 128) go(join_kernel<_Float16, 128>);
-    else go(join_kernel<_Float16, 64>);
+    if (a.c.dim == 256) go(few ? join_few_kernel<_Float16, 256> : join_kernel<_Float16, 256>);
+    else if (a.c.dim == 128) go(few ? join_few_kernel<_Float16, 128> : join_kernel<_Float16, 128>);
+    else go(few ? join_few_kernel<_Float16, 64> : join_kernel<_Float16, 64>);
   }
   return hipGetLastError();
 }

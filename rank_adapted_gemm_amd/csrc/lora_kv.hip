@@ -76,10 +76,179 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / 64;
 
-// One block per (sequence, head): the threshold of the budget's heaviest
-// positions by radix selection, eight key bits a pass, then the kept positions
-// in order.
+// The kept positions are those whose key is above the budget's last one, and the
+// first of those equal to it.  That key is found by radix selection: a histogram
+// of its top bits in LDS, the bin that holds the budget's end, then the next bits
+// among the keys of that bin.  One block takes one (sequence, head).
+
+// Finds the bin, counting from the highest of n (2 a thread), where `k` keys are reached;
+// sel[0] = the bin, sel[1] = how many of its keys are among the k.
+__device__ __forceinline__ void select_bin(const uint32_t* hist, int n, uint32_t k, uint32_t* wave_sum, uint32_t* sel) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int b = n - 1 - 2 * tid;
+  const uint32_t c0 = b > 0 ? hist[b] : 0, c1 = b > 0 ? hist[b - 1] : 0;
+  uint32_t upto = c0 + c1;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t o = __shfl_up(upto, d);
+    if (lane >= d) upto += o;
+  }
+  if (lane == 63) wave_sum[wave] = upto;
+  __syncthreads();
+  uint32_t before = upto - c0 - c1;   // keys in higher bins
+#pragma unroll
+  for (int w = 0; w < kSelWaves; ++w) before += w < wave ? wave_sum[w] : 0;
+  if (before < k && before + c0 >= k) {
+    sel[0] = uint32_t(b);
+    sel[1] = k - before;
+  } else if (before + c0 < k && before + c0 + c1 >= k) {
+    sel[0] = uint32_t(b - 1);
+    sel[1] = k - before - c0;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void keep_all(const EvictArgs& a, int len, const float* m, int32_t* kept, float* mout) {
+  for (int p = threadIdx.x; p < a.budget; p += kSelThreads) {
+    kept[p] = p < len ? p : -1;
+    if (mout) mout[p] = p < len ? m[p] : 0.0f;
+  }
+}
+
+// Keys stay in registers, four consecutive positions a thread in each of G groups of 4,096: the weights
+// are read once.  Digits of 11, 11 and 10 bits: with the sign, the exponent and two bits of the mantissa
+// in the first, weights of usual spread fall on enough bins that lanes seldom meet in one.
+template <int G>
 __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(EvictArgs a) {
+  __shared__ uint32_t hist[2048];
+  __shared__ uint32_t sel[2], wave_sum[kSelWaves];
+  __shared__ int2 count[G * kSelWaves];   // (above, equal) of a wave's 256 positions, then of all before them
+  typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+  const int i = blockIdx.x / a.c.kv_heads;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int len = a.s.kv_len[i];
+  const float* m = a.mass + int64_t(blockIdx.x) * a.mass_cap;
+  int32_t* kept = a.kept + int64_t(blockIdx.x) * a.budget;
+  float* mout = a.mass_out ? a.mass_out + int64_t(blockIdx.x) * a.budget : nullptr;
+  if (len <= a.budget) {
+    keep_all(a, len, m, kept, mout);
+    return;
+  }
+  const int lo = a.sinks, hi = len - a.recent;
+  const int want = a.budget - a.sinks - a.recent;
+  uint32_t key[G][4];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int p = (g * kSelThreads + tid) * 4;
+    f32x4u v = {0, 0, 0, 0};
+    if (p + 3 < len) {
+      v = *reinterpret_cast<const f32x4u*>(m + p);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (p + e < len) v[e] = m[p + e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) key[g][e] = mass_key(v[e]);
+  }
+  uint32_t prefix = 0, mask = 0, k = uint32_t(want);
+  if (want > 0) {
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : 2048;
+      hist[tid] = 0;
+      hist[tid + 1024] = 0;
+      __syncthreads();
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int p = (g * kSelThreads + tid) * 4 + e;
+          if (p >= lo && p < hi && (key[g][e] & mask) == prefix)
+            atomicAdd(&hist[(key[g][e] >> shift) & uint32_t(bins - 1)], 1u);
+        }
+      __syncthreads();
+      select_bin(hist, bins, k, wave_sum, sel);
+      prefix |= sel[0] << shift;
+      mask |= uint32_t(bins - 1) << shift;
+      k = sel[1];
+    }
+  }
+  // keys above the prefix are kept, and the first k equal to it
+  auto above = [&](int p, uint32_t x) { return p < len && (p < lo || p >= hi || (want > 0 && x > prefix)); };
+  auto equal = [&](int p, uint32_t x) { return p >= lo && p < hi && want > 0 && x == prefix; };
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    int na = 0, ne = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int p = (g * kSelThreads + tid) * 4 + e;
+      na += __popcll(__ballot(above(p, key[g][e])));
+      ne += __popcll(__ballot(equal(p, key[g][e])));
+    }
+    if (lane == 0) count[g * kSelWaves + wave] = int2{na, ne};
+  }
+  __syncthreads();
+  if (wave == 0) {
+    constexpr int PER = (G * kSelWaves + 63) / 64;
+    int2 c[PER], sum{0, 0};
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int at = lane * PER + e;
+      c[e] = at < G * kSelWaves ? count[at] : int2{0, 0};
+      sum.x += c[e].x;
+      sum.y += c[e].y;
+    }
+    int2 upto = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int ox = __shfl_up(upto.x, d), oy = __shfl_up(upto.y, d);
+      if (lane >= d) {
+        upto.x += ox;
+        upto.y += oy;
+      }
+    }
+    int2 at0{upto.x - sum.x, upto.y - sum.y};
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int at = lane * PER + e;
+      if (at < G * kSelWaves) count[at] = at0;
+      at0.x += c[e].x;
+      at0.y += c[e].y;
+    }
+  }
+  __syncthreads();
+  const uint64_t below = (uint64_t(1) << lane) - 1;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int2 base = count[g * kSelWaves + wave];
+    int na = base.x, ne = base.y;   // above and equal before this thread's position
+    bool is_a[4], is_e[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int p = (g * kSelThreads + tid) * 4 + e;
+      is_a[e] = above(p, key[g][e]);
+      is_e[e] = equal(p, key[g][e]);
+      na += __popcll(__ballot(is_a[e]) & below);
+      ne += __popcll(__ballot(is_e[e]) & below);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int p = (g * kSelThreads + tid) * 4 + e;
+      if (is_a[e] || (is_e[e] && uint32_t(ne) < k)) {
+        const int at = na + min(ne, int(k));
+        kept[at] = p;
+        if (mout) mout[at] = m[p];
+      }
+      na += is_a[e];
+      ne += is_e[e];
+    }
+  }
+}
+
+// Sequences of more positions than registers hold: every pass reads the weights again, eight key bits a
+// pass, and the kept positions leave in order.
+__global__ __launch_bounds__(kSelThreads) void evict_select_long_kernel(EvictArgs a) {
   __shared__ uint32_t hist[256];
   __shared__ uint32_t sel[2];
   __shared__ int wave_eq[kSelWaves], wave_keep[kSelWaves];
@@ -91,10 +260,7 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(EvictArgs a) 
   float* mout = a.mass_out ? a.mass_out + int64_t(blockIdx.x) * a.budget : nullptr;
 
   if (len <= a.budget) {
-    for (int p = tid; p < a.budget; p += kSelThreads) {
-      kept[p] = p < len ? p : -1;
-      if (mout) mout[p] = p < len ? m[p] : 0.0f;
-    }
+    keep_all(a, len, m, kept, mout);
     return;
   }
 
@@ -231,7 +397,14 @@ hipError_t launch_kv_append(const AppendArgs& a, int dtype, int cache_dtype, hip
 
 hipError_t launch_kv_evict(const EvictArgs& a, int cache_dtype, hipStream_t stream) {
   const int pairs = a.s.n * a.c.kv_heads;
-  hipLaunchKernelGGL(evict_select_kernel, dim3(pairs), dim3(kSelThreads), 0, stream, a);
+  int longest = 0;
+  for (int i = 0; i < a.s.n; ++i) longest = a.s.kv_len[i] > longest ? a.s.kv_len[i] : longest;
+  auto select = [&](auto* kernel) { hipLaunchKernelGGL(kernel, dim3(pairs), dim3(kSelThreads), 0, stream, a); };
+  if (longest <= 4096) select(evict_select_kernel<1>);
+  else if (longest <= 2 * 4096) select(evict_select_kernel<2>);
+  else if (longest <= 4 * 4096) select(evict_select_kernel<4>);
+  else if (longest <= 8 * 4096) select(evict_select_kernel<8>);
+  else select(evict_select_long_kernel);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   int kept = 0;
