@@ -6,8 +6,10 @@
 // four waves take 32 positions each in turn, every one through an LDS ring of
 // its own that DMA loads fill, so no wave waits for another before the end.  A
 // wave waits for a step's keys, multiplies, refills them, waits for its values,
-// multiplies and refills those: with 256-wide 16-bit rows the ring is one step
-// deep and half of a wave's 32 KiB are under way at any time.  S^T = K Q^T and
+// multiplies and refills those, so half of its ring or more is under way at any
+// time.  A ring takes 16 KiB (one to four steps), and two blocks share a CU, so
+// that one's start falls into the other's stream; 256-wide 16-bit rows take
+// 32 KiB a step and the CU alone.  S^T = K Q^T and
 // O^T = V^T P^T run on 16 x 16 x 32 MFMAs as in the prompts' kernel.  The waves
 // join in LDS; items that share rows leave sums in the workspace for the join.
 #include "lora_attn_core.h"
@@ -16,7 +18,7 @@ namespace lora {
 namespace {
 
 constexpr int kStep = 1 << kDecodeUnitShift;
-constexpr int kWaves = 4;
+constexpr int kWaves = kDecodeWaves;
 
 // Values of a fragment: lane's column d = db * 16 + (lane & 15) and the eight positions that its
 // registers of weights stand for: 4 (lane >> 4) + 0..3, and the same past 16.
@@ -62,15 +64,14 @@ struct ValueReader16 {
 
 // QT: 16-row columns of packed rows.  MASS: scores go to the workspace.
 template <typename T, bool F8, int DIM, int QT, bool MASS>
-__global__ __launch_bounds__(kWaves * 64, 1) void decode_kernel(AttnArgs a, AttnPart part) {
+__global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16)) void decode_kernel(AttnArgs a, AttnPart part) {
   using R = Row<F8, DIM>;
   using x8 = typename Vec<T>::x8;
   constexpr int BM = QT * 16, KS = DIM / 32, DB = DIM / 16, STEP = kStep * R::kBytes;   // STEP: bytes of a step's keys
-  constexpr int NS = STEP >= 16384 ? 1 : (STEP >= 8192 ? 2 : 4);                        // steps in a wave's ring
+  constexpr int NS = STEP >= 8192 ? 1 : (STEP >= 4096 ? 2 : 4);                         // steps in a wave's ring
   constexpr int NL = 2 * R::kLoads;                                                     // loads of a step's keys
-  constexpr int RING = 2 * NS * STEP;
-  constexpr int JOIN = BM * (DIM + 4) * 4;                                              // a wave's outputs at the end
-  constexpr int WAVE_LDS = RING > JOIN ? RING : JOIN;
+  constexpr int WAVE_LDS = decode_wave_lds(DIM, F8 ? 1 : 2, BM);                        // its ring, its outputs at the end
+  static_assert(WAVE_LDS >= 2 * NS * STEP && WAVE_LDS >= BM * (DIM + 4) * 4, "a wave's share of the LDS");
   __shared__ __attribute__((aligned(1024))) char lds[kWaves * WAVE_LDS];
   __shared__ float ml[kWaves][BM][2];
 
@@ -340,108 +341,164 @@ __global__ __launch_bounds__(kWaves * 64, 1) void decode_kernel(AttnArgs a, Attn
 
 // ---------------------------------------------------------------- join
 //
-// Bound by the sums it reads.  The item of split s takes the tile's rows s, s + nsplit, ..., so that all
-// items of a tile share the work.  Few splits: a wave a row, all of its loads under way at once.
+// Bound by the sums it reads.  All items of a tile share its rows.  Few splits (prompts): four columns a
+// thread, all of a row's loads under way at once.
 constexpr int kJoinFew = 8;
 
-struct JoinRow {
-  int64_t slot, step;   // the row's place in the first split's sums; from one split to the next
-  int64_t row;          // (row, head) of the output
-  int nsplit, head;
-  bool valid;
-};
-
-__device__ __forceinline__ JoinRow join_row(const AttnArgs& a, const AttnPart& part, int tile_rows, int nth) {
+template <typename T, int DIM>
+__global__ __launch_bounds__(256) void join_few_kernel(AttnArgs a, AttnPart part, int tile_rows, bool f8) {
+  constexpr int LANES = DIM / 4, ROWS = 256 / LANES;   // four columns a lane: 4 to 16 rows at a time
+  const int tid = threadIdx.x, sub = tid / LANES, d = (tid - sub * LANES) * 4;
   const int s = seq_of_item(part, blockIdx.x);
   const AttnSeq sq = part.seq[s];
   const int first = s == 0 ? 0 : part.seq[s - 1].item_end;
   const int M = sq.rows * a.group, tiles = (M - 1) / tile_rows + 1;
   const AttnItem item = attn_item(int(blockIdx.x) - first, a.c.kv_heads, sq.nsplit, tiles);
-  const int r = item.split + sq.nsplit * nth, m = item.tile * tile_rows + r;
-  JoinRow o;
-  o.valid = r < tile_rows && r < M - item.tile * tile_rows;
-  o.slot = (int64_t(blockIdx.x) - item.split * a.c.kv_heads) * tile_rows + r;
-  o.step = int64_t(a.c.kv_heads) * tile_rows;
-  const int j = m / a.group;
-  o.row = int64_t(sq.q_start + j) * a.heads + (m - j * a.group) + item.head * a.group;
-  o.nsplit = sq.nsplit;
-  o.head = item.head;
-  return o;
+  const int rows = min(tile_rows, M - item.tile * tile_rows);
+  const int64_t tile0 = (int64_t(blockIdx.x) - item.split * a.c.kv_heads) * tile_rows;
+  const int64_t step = int64_t(a.c.kv_heads) * tile_rows;
+  const float vs = f8 ? a.c.v_scale[item.head] : 1.0f;
+  // the rows of the item: a run of a share of the tile
+  const int per = (rows + sq.nsplit - 1) / sq.nsplit, r1 = min(rows, (item.split + 1) * per);
+  for (int r = item.split * per + int(blockIdx.y) * ROWS + sub; r < r1; r += int(gridDim.y) * ROWS) {
+    f32x4 o[kJoinFew];
+    f32x2 ml[kJoinFew];
+#pragma unroll
+    for (int i = 0; i < kJoinFew; ++i) {
+      if (i >= sq.nsplit) continue;
+      const int64_t slot = tile0 + r + i * step;
+      ml[i] = *reinterpret_cast<const f32x2*>(a.part_ml + slot * 2);
+      o[i] = *reinterpret_cast<const f32x4*>(a.part_o + slot * DIM + d);
+    }
+    float top = ml[0][0];
+#pragma unroll
+    for (int i = 1; i < kJoinFew; ++i)
+      if (i < sq.nsplit) top = __builtin_fmaxf(top, ml[i][0]);
+    float total = 0;
+    f32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kJoinFew; ++i) {
+      if (i >= sq.nsplit) continue;
+      const float f = __builtin_amdgcn_exp2f(ml[i][0] - top);
+      total += ml[i][1] * f;
+      sum += o[i] * f;
+    }
+    const float inv = total == 0 ? 0.0f : vs / total;
+    const int m = item.tile * tile_rows + r, j = m / a.group;
+    const int64_t row = int64_t(sq.q_start + j) * a.heads + (m - j * a.group) + item.head * a.group;
+    *reinterpret_cast<u32x2*>(a.out + (row * DIM + d) * 2) =
+        u32x2{pack_pair<T>(sum[0] * inv, sum[1] * inv), pack_pair<T>(sum[2] * inv, sum[3] * inv)};
+    if (a.lse && d == 0) a.lse[row] = total == 0 ? -INFINITY : top + __builtin_log2f(total);
+  }
 }
 
+// One row by a block: each of its four waves reads a quarter of the splits.
 template <typename T, int DIM>
-__global__ __launch_bounds__(256) void join_few_kernel(AttnArgs a, AttnPart part, int tile_rows, bool f8) {
-  constexpr int PER = DIM / 64;
-  typedef float vec __attribute__((ext_vector_type(PER)));
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const JoinRow x = join_row(a, part, tile_rows, int(blockIdx.y) * 4 + wave);
-  if (!x.valid) return;
-  vec o[kJoinFew];
-  f32x2 ml[kJoinFew];
-#pragma unroll
-  for (int i = 0; i < kJoinFew; ++i) {
-    const int64_t slot = x.slot + (i < x.nsplit ? i : 0) * x.step;   // past the end: the first again
-    ml[i] = *reinterpret_cast<const f32x2*>(a.part_ml + slot * 2);
-    o[i] = *reinterpret_cast<const vec*>(a.part_o + slot * DIM + lane * PER);
-  }
-  float top = ml[0][0];
-#pragma unroll
-  for (int i = 1; i < kJoinFew; ++i) top = __builtin_fmaxf(top, ml[i][0]);
-  float total = 0;
-  vec sum = {};
-#pragma unroll
-  for (int i = 0; i < kJoinFew; ++i) {
-    if (i >= x.nsplit) continue;
-    const float f = exp2f(ml[i][0] - top);
-    total += ml[i][1] * f;
-    sum += o[i] * f;
-  }
-  const float inv = total == 0 ? 0.0f : (f8 ? a.c.v_scale[x.head] : 1.0f) / total;
-  T* dst = reinterpret_cast<T*>(a.out) + x.row * DIM + lane * PER;
-  if constexpr (PER == 4)
-    *reinterpret_cast<u32x2*>(dst) = u32x2{pack_pair<T>(sum[0] * inv, sum[1] * inv), pack_pair<T>(sum[2] * inv, sum[3] * inv)};
-  else if constexpr (PER == 2)
-    *reinterpret_cast<uint32_t*>(dst) = pack_pair<T>(sum[0] * inv, sum[1] * inv);
-  else
-    *dst = T(sum[0] * inv);
-  if (a.lse && lane == 0) a.lse[x.row] = total == 0 ? -INFINITY : top + __builtin_log2f(total);
-}
-
-// Many splits: a block a row, each of its four waves a quarter of the splits.
-template <typename T, int DIM>
-__global__ __launch_bounds__(256) void join_kernel(AttnArgs a, AttnPart part, int tile_rows, bool f8) {
+__device__ __forceinline__ void join_one(const AttnArgs& a, const AttnSeq& sq, int64_t slot0, int64_t step, int head, int m,
+                                         bool f8) {
   constexpr int PER = DIM / 64;
   typedef float vec __attribute__((ext_vector_type(PER)));
   __shared__ float acc[4][DIM];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const JoinRow r = join_row(a, part, tile_rows, blockIdx.y);
-  if (!r.valid) return;
   float top = kLowest;
-  for (int i = lane; i < r.nsplit; i += 64) top = __builtin_fmaxf(top, a.part_ml[(r.slot + i * r.step) * 2]);
+  for (int i = lane; i < sq.nsplit; i += 64) top = __builtin_fmaxf(top, a.part_ml[(slot0 + i * step) * 2]);
   for (int d = 1; d < 64; d <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
   float total = 0;
-  for (int i = lane; i < r.nsplit; i += 64) {
-    const f32x2 x = *reinterpret_cast<const f32x2*>(a.part_ml + (r.slot + i * r.step) * 2);
-    total += x[1] * exp2f(x[0] - top);
+  for (int i = lane; i < sq.nsplit; i += 64) {
+    const f32x2 x = *reinterpret_cast<const f32x2*>(a.part_ml + (slot0 + i * step) * 2);
+    total += x[1] * __builtin_amdgcn_exp2f(x[0] - top);
   }
   for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
   vec sum = {};
 #pragma unroll 4
-  for (int i = wave; i < r.nsplit; i += 4) {
-    const int64_t slot = r.slot + i * r.step;
-    sum += *reinterpret_cast<const vec*>(a.part_o + slot * DIM + lane * PER) * exp2f(a.part_ml[slot * 2] - top);
+  for (int i = wave; i < sq.nsplit; i += 4) {
+    const int64_t slot = slot0 + i * step;
+    sum += *reinterpret_cast<const vec*>(a.part_o + slot * DIM + lane * PER) *
+           __builtin_amdgcn_exp2f(a.part_ml[slot * 2] - top);
   }
   *reinterpret_cast<vec*>(&acc[wave][lane * PER]) = sum;
   __syncthreads();
-  const float inv = total == 0 ? 0.0f : (f8 ? a.c.v_scale[r.head] : 1.0f) / total;
+  const int j = m / a.group;
+  const int64_t row = int64_t(sq.q_start + j) * a.heads + (m - j * a.group) + head * a.group;
+  const float inv = total == 0 ? 0.0f : (f8 ? a.c.v_scale[head] : 1.0f) / total;
   if (tid < DIM / 2) {
     float x[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       x[e] = (acc[0][2 * tid + e] + acc[1][2 * tid + e] + acc[2][2 * tid + e] + acc[3][2 * tid + e]) * inv;
-    *reinterpret_cast<uint32_t*>(a.out + (r.row * DIM + 2 * tid) * 2) = pack_pair<T>(x[0], x[1]);
+    *reinterpret_cast<uint32_t*>(a.out + (row * DIM + 2 * tid) * 2) = pack_pair<T>(x[0], x[1]);
   }
-  if (a.lse && tid == 0) a.lse[r.row] = total == 0 ? -INFINITY : top + __builtin_log2f(total);
+  if (a.lse && tid == 0) a.lse[row] = total == 0 ? -INFINITY : top + __builtin_log2f(total);
+}
+
+// Many splits: a block a row.
+template <typename T, int DIM>
+__global__ __launch_bounds__(256) void join_kernel(AttnArgs a, AttnPart part, int tile_rows, bool f8) {
+  const int s = seq_of_item(part, blockIdx.x);
+  const AttnSeq sq = part.seq[s];
+  const int first = s == 0 ? 0 : part.seq[s - 1].item_end;
+  const int M = sq.rows * a.group, tiles = (M - 1) / tile_rows + 1;
+  const AttnItem item = attn_item(int(blockIdx.x) - first, a.c.kv_heads, sq.nsplit, tiles);
+  const int r = item.split + sq.nsplit * int(blockIdx.y);
+  if (r >= tile_rows || r >= M - item.tile * tile_rows) return;
+  join_one<T, DIM>(a, sq, (int64_t(blockIdx.x) - item.split * a.c.kv_heads) * tile_rows + r,
+                   int64_t(a.c.kv_heads) * tile_rows, item.head, item.tile * tile_rows + r, f8);
+}
+
+// ---------------------------------------------------------------- accumulated weights of decoded rows
+//
+// One launch joins the rows and gives each position its weight: a thread a position, the scores that the
+// rows' items left in the workspace against the rows' totals.  blockIdx.x: `weight_blocks` runs of 256
+// positions, then a row each.
+template <typename T, int DIM>
+__global__ __launch_bounds__(256) void decode_finish_kernel(AttnArgs a, AttnPart part, int tile_rows, bool f8,
+                                                            int weight_blocks) {
+  __shared__ float lse[kAttnDecodeMaxRows];
+  const int s = blockIdx.z, head = blockIdx.y;
+  const AttnSeq sq = part.seq[s];
+  const int first = s == 0 ? 0 : part.seq[s - 1].item_end;
+  const int M = sq.rows * a.group;
+  const int64_t slot0 = (int64_t(first) + head) * tile_rows, step = int64_t(a.c.kv_heads) * tile_rows;
+  if (int(blockIdx.x) >= weight_blocks) {
+    const int m = int(blockIdx.x) - weight_blocks;
+    if (sq.nsplit > 1 && m < M) join_one<T, DIM>(a, sq, slot0 + m, step, head, m, f8);
+    return;
+  }
+  const int b0 = int(blockIdx.x) * 256;
+  if (b0 >= sq.kv_len) return;
+  const Units units = units_of(sq.kv_len - sq.rows, sq.kv_len - 1, a.window, a.sinks, kDecodeUnitShift);
+  const int p = b0 + threadIdx.x, unit = p >> kDecodeUnitShift;
+  const int u = unit < units.sinks ? unit : unit - units.gap;
+  const bool met = p < sq.kv_len && (unit < units.sinks || (u >= units.sinks && u < units.count));
+  float sum = 0;
+  if (__syncthreads_or(met)) {   // some position of the run is seen
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int m = wave; m < M; m += 4) {
+      float top = kLowest, total = 0;
+      for (int i = lane; i < sq.nsplit; i += 64) top = __builtin_fmaxf(top, a.part_ml[(slot0 + m + i * step) * 2]);
+      for (int d = 1; d < 64; d <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
+      for (int i = lane; i < sq.nsplit; i += 64) {
+        const f32x2 x = *reinterpret_cast<const f32x2*>(a.part_ml + (slot0 + m + i * step) * 2);
+        total += x[1] * __builtin_amdgcn_exp2f(x[0] - top);
+      }
+      for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+      if (lane == 0) lse[m] = total == 0 ? INFINITY : top + __builtin_log2f(total);   // nothing seen: no weight
+    }
+    __syncthreads();
+    if (met) {
+      const int split = int((int64_t(u + 1) * sq.nsplit - 1) / units.count);
+      const float* sc = a.scores + (int64_t(first) + split * a.c.kv_heads + head) * a.score_rows * part.score_cols +
+                        (u - split_begin(units.count, split, sq.nsplit)) * kStep + (p & (kStep - 1));
+#pragma unroll 4
+      for (int m = 0; m < M; ++m) {
+        const float x = sc[int64_t(m) * part.score_cols];
+        sum += x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(x - lse[m]);   // -inf: not seen
+      }
+    }
+  }
+  if (p >= sq.kv_len) return;
+  const int64_t at = (int64_t(sq.index) * a.c.kv_heads + head) * a.mass_cap + p;
+  a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.0f) + sum;
 }
 
 template <typename T, bool F8, int DIM, int QT>
@@ -464,51 +521,6 @@ void run_rows(const AttnArgs& a, const AttnPart& p, int rows, hipStream_t stream
   else run_dim<T, F8, 2>(a, p, stream);
 }
 
-// ---------------------------------------------------------------- accumulated weights of decoded rows
-//
-// A thread a position: the scores that the rows' items left in the workspace against the rows' totals.
-__global__ __launch_bounds__(256) void decode_mass_kernel(AttnArgs a, AttnPart part, int tile_rows) {
-  __shared__ float lse[kAttnDecodeMaxRows];
-  const int s = blockIdx.z, head = blockIdx.y;
-  const AttnSeq sq = part.seq[s];
-  const int first = s == 0 ? 0 : part.seq[s - 1].item_end;
-  if (int(blockIdx.x) * 256 >= sq.kv_len) return;
-  const int M = sq.rows * a.group;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int m = wave; m < M; m += 4) {
-    float top = kLowest, total = 0;
-    for (int i = lane; i < sq.nsplit; i += 64)
-      top = __builtin_fmaxf(top, a.part_ml[((int64_t(first) + i * a.c.kv_heads + head) * tile_rows + m) * 2]);
-    for (int d = 1; d < 64; d <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
-    for (int i = lane; i < sq.nsplit; i += 64) {
-      const f32x2 x = *reinterpret_cast<const f32x2*>(
-          a.part_ml + ((int64_t(first) + i * a.c.kv_heads + head) * tile_rows + m) * 2);
-      total += x[1] * exp2f(x[0] - top);
-    }
-    for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
-    if (lane == 0) lse[m] = total == 0 ? INFINITY : top + __builtin_log2f(total);   // no position seen: no weight
-  }
-  __syncthreads();
-  const int p = blockIdx.x * 256 + threadIdx.x;
-  if (p >= sq.kv_len) return;
-  const int64_t at = (int64_t(sq.index) * a.c.kv_heads + head) * a.mass_cap + p;
-  float sum = 0;
-  const Units units = units_of(sq.kv_len - sq.rows, sq.kv_len - 1, a.window, a.sinks, kDecodeUnitShift);
-  const int unit = p >> kDecodeUnitShift;
-  const int u = unit < units.sinks ? unit : unit - units.gap;
-  if (unit < units.sinks || (u >= units.sinks && u < units.count)) {
-    const int split = int((int64_t(u + 1) * sq.nsplit - 1) / units.count);
-    const int b = first + split * a.c.kv_heads + head;
-    const float* sc = a.scores + int64_t(b) * a.score_rows * part.score_cols +
-                      (u - split_begin(units.count, split, sq.nsplit)) * kStep + (p & (kStep - 1));
-    for (int m = 0; m < M; ++m) {
-      const float x = sc[int64_t(m) * part.score_cols];
-      sum += x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(x - lse[m]);   // -inf: not seen
-    }
-  }
-  a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.0f) + sum;
-}
-
 }  // namespace
 
 hipError_t launch_attn_decode(const AttnArgs& a, const AttnPart& p, int rows, int dtype, int cache_dtype,
@@ -524,32 +536,47 @@ hipError_t launch_attn_decode(const AttnArgs& a, const AttnPart& p, int rows, in
   return hipGetLastError();
 }
 
+namespace {
+
+// go(kernel) with K<T, DIM> for the call's type and head width.
+#define LORA_FOR_SHAPE(K, dtype, dim)                   \
+  do {                                                  \
+    if ((dtype) == LORA_KV_BF16) {                      \
+      if ((dim) == 256) go(K<__bf16, 256>);             \
+      else if ((dim) == 128) go(K<__bf16, 128>);        \
+      else go(K<__bf16, 64>);                           \
+    } else {                                            \
+      if ((dim) == 256) go(K<_Float16, 256>);           \
+      else if ((dim) == 128) go(K<_Float16, 128>);      \
+      else go(K<_Float16, 64>);                         \
+    }                                                   \
+  } while (0)
+
+}  // namespace
+
 hipError_t launch_attn_join(const AttnArgs& a, const AttnPart& p, int tile_rows, int most, int dtype,
                             hipStream_t stream) {
   int splits = 0;
   for (int i = 0; i < p.n; ++i) splits = p.seq[i].nsplit > splits ? p.seq[i].nsplit : splits;
-  const bool few = splits <= kJoinFew;
-  const dim3 grid(p.split_items, few ? (most + 3) / 4 : most), block(256);
-  const bool f8 = a.c.v_scale != nullptr;
+  const bool few = splits <= kJoinFew, f8 = a.c.v_scale != nullptr;
+  // few splits: a block goes over up to four runs of rows
+  const int runs = (most + 1024 / a.c.dim * 4 - 1) / (1024 / a.c.dim * 4);
+  const dim3 grid(p.split_items, few ? runs : most), block(256);
   auto go = [&](auto* kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, p, tile_rows, f8); };
-  if (dtype == LORA_KV_BF16) {
-    if (a.c.dim == 256) go(few ? join_few_kernel<__bf16, 256> : join_kernel<__bf16, 256>);
-    else if (a.c.dim == 128) go(few ? join_few_kernel<__bf16, 128> : join_kernel<__bf16, 128>);
-    else go(few ? join_few_kernel<__bf16, 64> : join_kernel<__bf16, 64>);
-  } else {
-    if (a.c.dim == 256) go(few ? join_few_kernel<_Float16, 256> : join_kernel<_Float16, 256>);
-    else if (a.c.dim == 128) go(few ? join_few_kernel<_Float16, 128> : join_kernel<_Float16, 128>);
-    else go(few ? join_few_kernel<_Float16, 64> : join_kernel<_Float16, 64>);
-  }
+  if (few) LORA_FOR_SHAPE(join_few_kernel, dtype, a.c.dim);
+  else LORA_FOR_SHAPE(join_kernel, dtype, a.c.dim);
   return hipGetLastError();
 }
 
-hipError_t launch_attn_mass_decode(const AttnArgs& a, const AttnPart& p, int tile_rows, hipStream_t stream) {
+hipError_t launch_attn_decode_finish(const AttnArgs& a, const AttnPart& p, int tile_rows, int rows, int dtype,
+                                     hipStream_t stream) {
   int longest = 0;
   for (int i = 0; i < p.n; ++i) longest = p.seq[i].kv_len > longest ? p.seq[i].kv_len : longest;
-  if (longest == 0) return hipSuccess;
-  hipLaunchKernelGGL(decode_mass_kernel, dim3((longest + 255) / 256, a.c.kv_heads, p.n), dim3(256), 0, stream, a, p,
-                     tile_rows);
+  const int weights = (longest + 255) / 256;
+  const dim3 grid(weights + (p.split_items > 0 ? rows : 0), a.c.kv_heads, p.n), block(256);
+  const bool f8 = a.c.v_scale != nullptr;
+  auto go = [&](auto* kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, p, tile_rows, f8, weights); };
+  LORA_FOR_SHAPE(decode_finish_kernel, dtype, a.c.dim);
   return hipGetLastError();
 }
 

@@ -8,6 +8,7 @@
 namespace lora {
 
 constexpr int kAttnCUs = 256;
+constexpr int kAttnRideUnits = 64 * kAttnCUs;   // short sequences' steps in a prompt launch
 constexpr int kAttnParts = (LORA_MAX_SEGMENTS + kAttnSeqs - 1) / kAttnSeqs;
 
 // One kernel's sequences, in launches of at most kAttnSeqs.
@@ -31,9 +32,10 @@ struct AttnWork {
 
 // The longest run of units an item may take.  A launch that fits the chip at once ends with its longest
 // item; a larger one, dealt out from the longest, ends about half an item after an even share.  `each`
-// and `split` are what an item and what leaving sums in the workspace cost, `join` the join's launch.
+// and `split` are what an item and what leaving sums in the workspace cost, `join` the join's launch;
+// an item's waves take `grain` units at a time.
 inline int attn_chunk(const AttnWork* w, int n, int64_t kv_heads, int64_t slots, double each, double split,
-                      double join, int least) {
+                      double join, int least, int grain) {
   int top = 1;
   for (int i = 0; i < n; ++i) top = std::max(top, w[i].units_last);
   int best = top;
@@ -45,7 +47,8 @@ inline int attn_chunk(const AttnWork* w, int n, int64_t kv_heads, int64_t slots,
       const int ns = std::max(1, (w[i].units_last + c - 1) / c);
       const double count = double(w[i].tiles) * ns * kv_heads, over = each + (ns > 1 ? split : 0);
       total += count * over + 0.5 * (double(w[i].units_last) + w[i].units_first) * w[i].tiles * kv_heads;
-      longest = std::max(longest, (w[i].units_last + ns - 1) / ns + over);
+      const int run = (w[i].units_last + ns - 1) / ns;
+      longest = std::max(longest, (run + grain - 1) / grain * grain + over);
       items += count;
       any |= ns > 1;
     }
@@ -96,11 +99,21 @@ inline void attn_plan(AttnPlan& o, const KvView& c, const KvSeqs& s, int n_heads
   const int group = n_heads / c.kv_heads;
   o.decode_rows = 0;
   int64_t prompt_items = 0;
+  // Beside prompts, a few short sequences ride in their launch: a tile with one wave at work costs a step
+  // about as long as its bytes take, less than launches of their own.
+  int64_t short_units = 0;
+  bool prompts = false;
+  for (int i = 0; i < s.n; ++i) {
+    const int rows = s.q_start[i + 1] - s.q_start[i], len = s.kv_len[i];
+    if (int64_t(rows) * group > kAttnDecodeMaxRows) prompts = true;
+    else if (rows > 0) short_units += units_of(len - rows, len - 1, window, sinks, kPromptUnitShift).count;
+  }
+  const bool ride = prompts && short_units * c.kv_heads <= kAttnRideUnits;
   for (int i = 0; i < s.n; ++i) {
     const int rows = s.q_start[i + 1] - s.q_start[i], len = s.kv_len[i];
     if (rows == 0 && !(mass && len > 0)) continue;
     const int64_t packed = int64_t(rows) * group;
-    if (packed <= kAttnDecodeMaxRows) {
+    if (packed <= kAttnDecodeMaxRows && !(ride && rows > 0)) {
       const Units u = units_of(len - rows, len - 1, window, sinks, kDecodeUnitShift);
       dec[nd++] = AttnWork{i, rows, rows == 0 ? 1 : u.count, rows == 0 ? 0 : u.count, 1, 1};
       o.decode_rows = std::max(o.decode_rows, int(packed));
@@ -116,11 +129,13 @@ inline void attn_plan(AttnPlan& o, const KvView& c, const KvSeqs& s, int n_heads
   o.decode_tile = o.decode_rows <= 16 ? 16 : 32;
   // in units: 32 positions' keys and values of a head, against about 64 KiB a block's start costs
   const double unit_bytes = double(c.dim) * elem_bytes * 2 * (1 << kDecodeUnitShift);
-  const int dchunk = attn_chunk(dec, nd, c.kv_heads, kAttnCUs, 65536 / unit_bytes, 0, 98304 / unit_bytes, 8);
+  const int dblocks = decode_blocks(c.dim, elem_bytes, o.decode_tile);
+  const int dchunk = attn_chunk(dec, nd, c.kv_heads, dblocks * kAttnCUs, 65536 / unit_bytes, 0, 98304 / unit_bytes,
+                                kDecodeWaves, kDecodeWaves);
   attn_fill(o.decode, dec, nd, dchunk, s, c.kv_heads, o.decode_tile, group);
   // in units: 64 positions against 256 rows; a split item's sums are 256 fp32 rows written and read
   const int64_t slots = c.dim == 256 ? kAttnCUs : 2 * kAttnCUs;
-  const int pchunk = prompt_items >= 16 * slots ? 1 << 30 : attn_chunk(pro, np, c.kv_heads, slots, 3, 6, 2, 8);
+  const int pchunk = prompt_items >= 16 * slots ? 1 << 30 : attn_chunk(pro, np, c.kv_heads, slots, 3, 6, 2, 8, 1);
   attn_fill(o.prompt, pro, np, pchunk, s, c.kv_heads, kPromptRows, group);
 
   size_t rows_o = 0, rows_ml = 0, score = 0;

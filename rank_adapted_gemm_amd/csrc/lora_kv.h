@@ -156,8 +156,21 @@ constexpr int kDecodeUnitShift = 5;   // 32 positions, one wave's step
 constexpr int kPromptUnitShift = 6;   // 64 positions, one block's step
 constexpr int kAttnDecodeRows = 16;       // packed rows a decode tile holds for each 16-row column of the product
 constexpr int kAttnDecodeMaxRows = 32;    // sequences of at most that many packed rows are decoded
+constexpr int kDecodeWaves = 4;
 constexpr int kPromptRows = 256;      // packed rows of a prompt tile
 constexpr int kMassRows = 128;        // positions of a prompt's weight block
+
+// LDS of a decode wave: a ring of 16 KiB, or of one step's keys and values where those take 32, and at the
+// end its fp32 outputs, padded against bank conflicts.
+constexpr int decode_wave_lds(int dim, int elem_bytes, int tile_rows) {
+  const int step = 2 * dim * elem_bytes << kDecodeUnitShift, ring = step > 16384 ? step : 16384;
+  const int out = tile_rows * (dim + 4) * 4;
+  return ring > out ? ring : out;
+}
+// Decode blocks that share a CU's 160 KiB.
+constexpr int decode_blocks(int dim, int elem_bytes, int tile_rows) {
+  return kDecodeWaves * decode_wave_lds(dim, elem_bytes, tile_rows) <= 76 * 1024 ? 2 : 1;
+}
 
 hipError_t launch_kv_append(const AppendArgs& a, int dtype, int cache_dtype, hipStream_t stream);
 hipError_t launch_kv_evict(const EvictArgs& a, int cache_dtype, hipStream_t stream);
@@ -168,6 +181,7 @@ hipError_t launch_attn_join(const AttnArgs& a, const AttnPart& p, int tile_rows,
                             hipStream_t stream);
 hipError_t launch_attn_mass_prompt(const AttnArgs& a, const AttnPart& p, int dtype, int cache_dtype,
                                    hipStream_t stream);
-hipError_t launch_attn_mass_decode(const AttnArgs& a, const AttnPart& p, int tile_rows, hipStream_t stream);
+hipError_t launch_attn_decode_finish(const AttnArgs& a, const AttnPart& p, int tile_rows, int rows, int dtype,
+                                     hipStream_t stream);
 
 }  // namespace lora

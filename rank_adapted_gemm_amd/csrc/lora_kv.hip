@@ -77,16 +77,24 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / 64;
 
 // The kept positions are those whose key is above the budget's last one, and the
-// first of those equal to it.  That key is found by radix selection: a histogram
-// of its top bits in LDS, the bin that holds the budget's end, then the next bits
-// among the keys of that bin.  One block takes one (sequence, head).
+// first of those equal to it; first and last positions that stay anyway take the
+// highest key, which no weight has.  The last key is found by radix selection: a
+// histogram of its top bits in LDS, the bin that holds the budget's end, then the
+// next bits among the keys of that bin.  One block takes one (sequence, head).
+constexpr uint32_t kStays = 0xFFFFFFFFu;
 
 // Finds the bin, counting from the highest of n (2 a thread), where `k` keys are reached;
-// sel[0] = the bin, sel[1] = how many of its keys are among the k.
-__device__ __forceinline__ void select_bin(const uint32_t* hist, int n, uint32_t k, uint32_t* wave_sum, uint32_t* sel) {
+// sel[0] = the bin, sel[1] = how many of its keys are among the k.  The histogram is `copies` long ones.
+__device__ __forceinline__ void select_bin(const uint32_t* hist, int n, int copies, uint32_t k, uint32_t* wave_sum,
+                                           uint32_t* sel) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int b = n - 1 - 2 * tid;
-  const uint32_t c0 = b > 0 ? hist[b] : 0, c1 = b > 0 ? hist[b - 1] : 0;
+  uint32_t c0 = 0, c1 = 0;
+  if (b > 0)
+    for (int x = 0; x < copies; ++x) {
+      c0 += hist[x * n + b];
+      c1 += hist[x * n + b - 1];
+    }
   uint32_t upto = c0 + c1;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -116,26 +124,27 @@ __device__ __forceinline__ void keep_all(const EvictArgs& a, int len, const floa
 }
 
 // Keys stay in registers, four consecutive positions a thread in each of G groups of 4,096: the weights
-// are read once.  Digits of 11, 11 and 10 bits: with the sign, the exponent and two bits of the mantissa
-// in the first, weights of usual spread fall on enough bins that lanes seldom meet in one.
+// are read once.  Few pairs leave most CUs idle, so what counts is the instructions a key costs: about
+// 512 cycles each at G = 8.  Digits of 11, 11 and 10 bits: with the sign, the exponent and two bits of
+// the mantissa in the first, weights of usual spread fall on enough bins, and four copies of the
+// histogram keep lanes with equal weights (zeros above all) apart.
 template <int G>
 __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(EvictArgs a) {
-  __shared__ uint32_t hist[2048];
+  constexpr int kCopies = 4;
+  __shared__ uint32_t hist[kCopies * 2048];
   __shared__ uint32_t sel[2], wave_sum[kSelWaves];
-  __shared__ int2 count[G * kSelWaves];   // (above, equal) of a wave's 256 positions, then of all before them
+  __shared__ int2 count[G * kSelWaves];   // (above, at least equal) of a wave's 256 positions, then of all before them
   typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
   const int i = blockIdx.x / a.c.kv_heads;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int len = a.s.kv_len[i];
   const float* m = a.mass + int64_t(blockIdx.x) * a.mass_cap;
   int32_t* kept = a.kept + int64_t(blockIdx.x) * a.budget;
-  float* mout = a.mass_out ? a.mass_out + int64_t(blockIdx.x) * a.budget : nullptr;
   if (len <= a.budget) {
-    keep_all(a, len, m, kept, mout);
+    keep_all(a, len, m, kept, a.mass_out ? a.mass_out + int64_t(blockIdx.x) * a.budget : nullptr);
     return;
   }
   const int lo = a.sinks, hi = len - a.recent;
-  const int want = a.budget - a.sinks - a.recent;
   uint32_t key[G][4];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
@@ -150,43 +159,43 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(EvictArgs a) 
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) key[g][e] = mass_key(v[e]);
-  }
-  uint32_t prefix = 0, mask = 0, k = uint32_t(want);
-  if (want > 0) {
+    if (p < lo || p + 3 >= hi) {
+      // past the end: the lowest key, and behind every position that could tie with it
 #pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : 2048;
-      hist[tid] = 0;
-      hist[tid + 1024] = 0;
-      __syncthreads();
-#pragma unroll
-      for (int g = 0; g < G; ++g)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int p = (g * kSelThreads + tid) * 4 + e;
-          if (p >= lo && p < hi && (key[g][e] & mask) == prefix)
-            atomicAdd(&hist[(key[g][e] >> shift) & uint32_t(bins - 1)], 1u);
-        }
-      __syncthreads();
-      select_bin(hist, bins, k, wave_sum, sel);
-      prefix |= sel[0] << shift;
-      mask |= uint32_t(bins - 1) << shift;
-      k = sel[1];
+      for (int e = 0; e < 4; ++e)
+        key[g][e] = p + e >= len ? 0u : (p + e < lo || p + e >= hi ? kStays : key[g][e]);
     }
+  }
+  uint32_t prefix = 0, k = uint32_t(a.budget);   // the top bits so far; keys still to take among those that share them
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11, copies = pass == 0 ? kCopies : 1;
+    for (int x = tid; x < copies << bits; x += kSelThreads) hist[x] = 0;
+    __syncthreads();
+    uint32_t* mine = hist + (pass == 0 ? (lane & (kCopies - 1)) << bits : 0);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (g * 4 * kSelThreads >= len) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (pass == 0 || key[g][e] >> (shift + bits) == prefix)
+          atomicAdd(&mine[(key[g][e] >> shift) & ((1u << bits) - 1)], 1u);
+    }
+    __syncthreads();
+    select_bin(hist, 1 << bits, copies, k, wave_sum, sel);
+    prefix = prefix << bits | sel[0];
+    k = sel[1];
   }
   // keys above the prefix are kept, and the first k equal to it
-  auto above = [&](int p, uint32_t x) { return p < len && (p < lo || p >= hi || (want > 0 && x > prefix)); };
-  auto equal = [&](int p, uint32_t x) { return p >= lo && p < hi && want > 0 && x == prefix; };
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    int na = 0, ne = 0;
+    int above = 0, least = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int p = (g * kSelThreads + tid) * 4 + e;
-      na += __popcll(__ballot(above(p, key[g][e])));
-      ne += __popcll(__ballot(equal(p, key[g][e])));
+      above += __popcll(__ballot(key[g][e] > prefix));
+      least += __popcll(__ballot(key[g][e] >= prefix));
     }
-    if (lane == 0) count[g * kSelWaves + wave] = int2{na, ne};
+    if (lane == 0) count[g * kSelWaves + wave] = int2{above, least};
   }
   __syncthreads();
   if (wave == 0) {
@@ -218,31 +227,43 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(EvictArgs a) 
     }
   }
   __syncthreads();
-  const uint64_t below = (uint64_t(1) << lane) - 1;
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const int2 base = count[g * kSelWaves + wave];
-    int na = base.x, ne = base.y;   // above and equal before this thread's position
-    bool is_a[4], is_e[4];
+    const int at = g * kSelWaves + wave;
+    if (at * 256 >= len) continue;
+    const int above = __builtin_amdgcn_readfirstlane(count[at].x);
+    const int equal = __builtin_amdgcn_readfirstlane(count[at].y) - above;   // equal to the prefix, before the group
+    int to = above + min(equal, int(k));
+    const bool taken = equal >= int(k);   // all ties lie before the group
+    int here = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int p = (g * kSelThreads + tid) * 4 + e;
-      is_a[e] = above(p, key[g][e]);
-      is_e[e] = equal(p, key[g][e]);
-      na += __popcll(__ballot(is_a[e]) & below);
-      ne += __popcll(__ballot(is_e[e]) & below);
-    }
+    for (int e = 0; e < 4; ++e) here += __popcll(__ballot(key[g][e] == prefix));
+    bool stays[4];
+    if (!taken && equal + here > int(k)) {   // the last tie lies in it
+      int rank = equal;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int p = (g * kSelThreads + tid) * 4 + e;
-      if (is_a[e] || (is_e[e] && uint32_t(ne) < k)) {
-        const int at = na + min(ne, int(k));
-        kept[at] = p;
-        if (mout) mout[at] = m[p];
+      for (int e = 0; e < 4; ++e) {
+        const uint64_t b = __ballot(key[g][e] == prefix);
+        rank = __builtin_amdgcn_mbcnt_hi(uint32_t(b >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(b), rank));
       }
-      na += is_a[e];
-      ne += is_e[e];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool tie = key[g][e] == prefix;
+        stays[e] = key[g][e] > prefix || (tie && rank < int(k));
+        rank += tie;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) stays[e] = taken ? key[g][e] > prefix : key[g][e] >= prefix;
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t b = __ballot(stays[e]);
+      to = __builtin_amdgcn_mbcnt_hi(uint32_t(b >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(b), to));
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (stays[e]) kept[to++] = (g * kSelThreads + tid) * 4 + e;
   }
 }
 
@@ -257,10 +278,9 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_long_kernel(EvictArg
   const int len = a.s.kv_len[i];
   const float* m = a.mass + int64_t(blockIdx.x) * a.mass_cap;
   int32_t* kept = a.kept + int64_t(blockIdx.x) * a.budget;
-  float* mout = a.mass_out ? a.mass_out + int64_t(blockIdx.x) * a.budget : nullptr;
 
   if (len <= a.budget) {
-    keep_all(a, len, m, kept, mout);
+    keep_all(a, len, m, kept, a.mass_out ? a.mass_out + int64_t(blockIdx.x) * a.budget : nullptr);
     return;
   }
 
@@ -330,10 +350,7 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_long_kernel(EvictArg
       all += wave_keep[w];
     }
     at += __popcll(kb & below);
-    if (keep) {
-      kept[at] = p;
-      if (mout) mout[at] = v;
-    }
+    if (keep) kept[at] = p;
     eq_seen += all_eq;
     out += all;
     __syncthreads();
@@ -342,7 +359,7 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_long_kernel(EvictArg
 
 constexpr int kGatherRows = 64;
 
-// Copies kept rows to their new slots; blockIdx.y is (sequence, head).
+// Copies kept rows to their new slots, and their weights; blockIdx.y is (sequence, head).
 __global__ __launch_bounds__(256) void evict_gather_kernel(EvictArgs a, int elem_bytes, uint32_t nan_word) {
   __shared__ int64_t src[kGatherRows], dst[kGatherRows];   // byte offsets; -1: no row, -2: source page invalid
   const int i = blockIdx.y / a.c.kv_heads, h = blockIdx.y - i * a.c.kv_heads;
@@ -366,6 +383,9 @@ __global__ __launch_bounds__(256) void evict_gather_kernel(EvictArgs a, int elem
     }
     src[threadIdx.x] = so;
     dst[threadIdx.x] = to;
+    if (slot < n && a.mass_out && a.s.kv_len[i] > a.budget)   // a sequence kept whole has them already
+      a.mass_out[int64_t(blockIdx.y) * a.budget + slot] =
+          a.mass[int64_t(blockIdx.y) * a.mass_cap + a.kept[int64_t(blockIdx.y) * a.budget + slot]];
   }
   __syncthreads();
   const int per = a.c.dim * elem_bytes / 16;

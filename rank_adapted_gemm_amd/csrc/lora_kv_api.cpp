@@ -233,9 +233,10 @@ lora_status lora_attn(const lora_kv_cache* cache, const lora_kv_batch* batch,
   for (int i = 0; i < plan.decode.parts && e == hipSuccess; ++i) {
     const lora::AttnPart& p = plan.decode.part[i];
     if (p.items > 0) e = lora::launch_attn_decode(a, p, plan.decode_rows, dtype, cache->dtype, stream);
-    if (e == hipSuccess && p.split_items > 0)
+    if (e == hipSuccess && mass_out)
+      e = lora::launch_attn_decode_finish(a, p, plan.decode_tile, plan.decode_rows, dtype, stream);
+    else if (e == hipSuccess && p.split_items > 0)
       e = lora::launch_attn_join(a, p, plan.decode_tile, plan.decode.join_rows[i], dtype, stream);
-    if (e == hipSuccess && mass_out) e = lora::launch_attn_mass_decode(a, p, plan.decode_tile, stream);
   }
   a.lse = mass_out ? reinterpret_cast<float*>(ws + plan.off_lse) : nullptr;
   for (int i = 0; i < plan.prompt.parts && e == hipSuccess; ++i) {
