@@ -58,6 +58,11 @@ __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, typename Vec<T>::x2));
 }
 
+// A value that all lanes share, in a scalar register.
+__device__ __forceinline__ float uniform(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int32_t, x)));
+}
+
 __device__ __forceinline__ float max_halves(float x) {   // over lanes l and l ^ 32
   const uint32_t u = __builtin_bit_cast(uint32_t, x);
   const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
