@@ -119,6 +119,14 @@ def _row_code(cache, batch, name, t):
     return code
 
 
+def _handle(stream, cache):
+    """The raw stream a call is enqueued on: torch's current one on the cache's device, or `stream`."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(cache._index)
+    return _bd._stream_of(stream, cache.device).cuda_stream
+
+
 def _empty(shape, dtype, dev, stream):
     """A new tensor, allocated for the stream that writes it."""
     import torch
@@ -151,9 +159,8 @@ def kv_append(cache, batch, k, v, stream=None):
     if code != _row_code(cache, batch, "v", v) or k.shape != v.shape or k.shape[1] != cache.kv_heads or \
             strides != _strides3("v", v, cache.head_dim):
         raise ValueError("k and v must be (rows, kv_heads, head_dim) of one type and the same strides")
-    s = _bd._stream_of(stream, cache.device)
     _raise(_bd.load().lora_kv_append(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), strides[0], strides[1],
-                                     code, s.cuda_stream))
+                                     code, _handle(stream, cache)))
 
 
 def attn_workspace_bytes(cache, batch, heads, window=-1, sinks=0, mass=False):
@@ -169,7 +176,7 @@ def attn_workspace(cache, batch, heads, window=-1, sinks=0, mass=False, stream=N
     need = attn_workspace_bytes(cache, batch, heads, window, sinks, mass)
     if not need:
         return None
-    _bd._stream_of(stream, cache.device)
+    _handle(stream, cache)
     return _empty(need, torch.uint8, cache.device, stream)
 
 
@@ -186,7 +193,7 @@ def attn(cache, batch, q, scale=None, window=-1, sinks=0, out=None, mass=None, m
     strides = _strides3("q", q, cache.head_dim)
     heads = q.shape[1]
     dev = cache.device
-    s = _bd._stream_of(stream, dev)
+    s = _handle(stream, cache)
     if out is None:
         out = _empty(q.shape, q.dtype, dev, stream)
     elif out.dtype != q.dtype or out.device != dev or not out.is_contiguous() or out.shape != q.shape:
@@ -206,7 +213,7 @@ def attn(cache, batch, q, scale=None, window=-1, sinks=0, out=None, mass=None, m
         else (None, 0)
     _raise(_bd.load().lora_attn(cache._ref, batch._ref, q.data_ptr(), strides[0], strides[1], heads, code,
                                 cache.head_dim ** -0.5 if scale is None else float(scale), int(window), int(sinks),
-                                out.data_ptr(), m_in, m_out, cap, ws, ws_bytes, s.cuda_stream))
+                                out.data_ptr(), m_in, m_out, cap, ws, ws_bytes, s))
     return out
 
 
@@ -230,7 +237,7 @@ def kv_evict(cache, batch, mass, budget, dst_table, sinks=0, recent=0, kept=None
         raise ValueError(f"mass holds {cap} positions, the batch reaches {batch.max_len}")
     m_in = _mass_ptr("mass", mass, (batch.n_seq, cache.kv_heads, cap), dev)
     shape = (batch.n_seq, cache.kv_heads, max(budget, 0))
-    s = _bd._stream_of(stream, dev)
+    s = _handle(stream, cache)
     if kept is None:
         kept = _empty(shape, torch.int32, dev, stream)
     elif kept.dtype != torch.int32 or kept.device != dev or not kept.is_contiguous() or tuple(kept.shape) != shape:
@@ -239,5 +246,5 @@ def kv_evict(cache, batch, mass, budget, dst_table, sinks=0, recent=0, kept=None
         mass_out = _empty(shape, torch.float32, dev, stream)
     m_out = _mass_ptr("mass_out", mass_out, shape, dev)
     _raise(_bd.load().lora_kv_evict(cache._ref, batch._ref, m_in, cap, budget, int(sinks), int(recent),
-                                    dst_table.data_ptr(), dst_stride, kept.data_ptr(), m_out, s.cuda_stream))
+                                    dst_table.data_ptr(), dst_stride, kept.data_ptr(), m_out, s))
     return kept, mass_out

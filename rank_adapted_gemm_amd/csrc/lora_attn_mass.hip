@@ -14,7 +14,7 @@ namespace {
 constexpr int kQN = 64;   // packed rows of a step
 
 template <typename T, bool F8, int DIM>
-__global__ __launch_bounds__(256, 2) void prompt_mass_kernel(AttnArgs a, AttnPart part) {
+__global__ __launch_bounds__(256, DIM == 64 ? 4 : 2) void prompt_mass_kernel(AttnArgs a, AttnPart part) {
   using Q = Row<false, DIM>;   // rows of q are 16 bits wide whatever the cache holds
   using x8 = typename Vec<T>::x8;
   constexpr int KS = DIM / 16, TILE = kQN * Q::kBytes, NX = TILE / 16 / 256;   // 16-byte pieces of a step a thread

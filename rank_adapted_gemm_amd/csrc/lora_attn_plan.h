@@ -28,37 +28,119 @@ struct AttnPlan {
 // A sequence's work for one kernel.
 struct AttnWork {
   int index, rows, units_last, units_first, tiles, nsplit;
+  double weight;   // a unit's cost: a tile with few waves at work takes its steps faster
 };
 
-// The longest run of units an item may take.  A launch that fits the chip at once ends with its longest
-// item; a larger one, dealt out from the longest, ends about half an item after an even share.  `each`
-// and `split` are what an item and what leaving sums in the workspace cost, `join` the join's launch;
-// an item's waves take `grain` units at a time.
+// When a launch's items, dealt out from the longest to the slot that is free first, are all done.  Items
+// come in classes of one size; slots are kept in groups of one load.
+struct AttnDeal {
+  struct Load {
+    double at;
+    int64_t slots;
+  };
+  struct Size {
+    double size;
+    int64_t items;
+  };
+  static constexpr int kLoads = 24, kSizes = 64;
+  Size sizes[kSizes];
+  int n = 0;
+
+  void add(double size, int64_t items) {
+    if (items > 0 && n < kSizes) sizes[n++] = Size{size, items};
+  }
+  double finish(int64_t slots) {
+    std::sort(sizes, sizes + n, [](const Size& a, const Size& b) { return a.size > b.size; });
+    Load load[kLoads + 1];   // ascending
+    int loads = 1;
+    load[0] = Load{0, slots};
+    for (int i = 0; i < n; ++i) {
+      int64_t left = sizes[i].items;
+      if (left > 64 * slots) {   // many rounds: an even share
+        for (int l = 0; l < loads; ++l) load[l].at += sizes[i].size * double(left / slots);
+        left %= slots;
+      }
+      while (left > 0) {
+        const int64_t take = std::min(left, load[0].slots);
+        const Load next{load[0].at + sizes[i].size, take};
+        left -= take;
+        load[0].slots -= take;
+        const int from = load[0].slots == 0 ? 1 : 0;
+        int at = from;
+        while (at < loads && load[at].at < next.at) ++at;
+        // groups within a hundredth of each other become one
+        if (at < loads && load[at].at <= next.at * 1.01) {
+          load[at].slots += take;
+        } else if (at > from && load[at - 1].at * 1.01 >= next.at) {
+          load[at - 1].slots += take;
+          load[at - 1].at = next.at;
+        } else if (loads - from < kLoads) {
+          for (int l = loads; l > at; --l) load[l] = load[l - 1];
+          load[at] = next;
+          ++loads;
+        } else {
+          load[std::min(at, loads - 1)].slots += take;
+        }
+        if (from) {
+          for (int l = 1; l < loads; ++l) load[l - 1] = load[l];
+          --loads;
+        }
+      }
+    }
+    return load[loads - 1].at;
+  }
+};
+
+// The longest run of units an item may take, so that the launch ends soonest.  `each` and `split` are what
+// an item and what leaving sums in the workspace cost in units, `join` the join's launch; an item's waves
+// take `grain` units at a time.
 inline int attn_chunk(const AttnWork* w, int n, int64_t kv_heads, int64_t slots, double each, double split,
                       double join, int least, int grain) {
-  int top = 1;
-  for (int i = 0; i < n; ++i) top = std::max(top, w[i].units_last);
+  constexpr int kClasses = 12;   // sequences of similar length count as one class
+  struct Class {
+    double last, first, weight;
+    int64_t items;
+  };
+  Class cls[kClasses];
+  int classes = 0, top = 1;
+  double total = 0;
+  const int per = (n + kClasses - 1) / kClasses;
+  for (int i = 0; i < n; i += per, ++classes) {   // w: longest first
+    Class& k = cls[classes];
+    k = Class{0, 0, 0, 0};
+    const int m = std::min(per, n - i);
+    for (int j = i; j < i + m; ++j) {
+      k.last += double(w[j].units_last) / m;
+      k.first += double(w[j].units_first) / m;
+      k.weight += w[j].weight / m;
+      k.items += int64_t(w[j].tiles) * kv_heads;
+      top = std::max(top, w[j].units_last);
+      total += 0.5 * (double(w[j].units_last) + w[j].units_first) * w[j].tiles * kv_heads * w[j].weight;
+    }
+  }
   int best = top;
   double best_cost = 0;
-  for (int c = top;; c = std::max(least, int(c * 0.85))) {
-    double total = 0, longest = 0, items = 0;
+  for (int c = top;; c = std::max(least, int(c * 0.86))) {
+    AttnDeal deal;
     bool any = false;
-    for (int i = 0; i < n; ++i) {
-      const int ns = std::max(1, (w[i].units_last + c - 1) / c);
-      const double count = double(w[i].tiles) * ns * kv_heads, over = each + (ns > 1 ? split : 0);
-      total += count * over + 0.5 * (double(w[i].units_last) + w[i].units_first) * w[i].tiles * kv_heads;
-      const int run = (w[i].units_last + ns - 1) / ns;
-      longest = std::max(longest, (run + grain - 1) / grain * grain + over);
-      items += count;
+    for (int i = 0; i < classes; ++i) {
+      const Class& k = cls[i];
+      const int64_t ns = std::max<int64_t>(1, int64_t(k.last + c - 1) / c);
       any |= ns > 1;
+      const double over = each + (ns > 1 ? split : 0);
+      const int parts = k.first < 0.75 * k.last ? 4 : 1;   // a causal prompt's tiles differ
+      for (int q = 0; q < parts; ++q) {
+        const double units = parts == 1 ? k.last : k.first + (k.last - k.first) * (q + 0.5) / parts;
+        const double run = double(int64_t((units / ns + grain - 0.01) / grain)) * grain;
+        deal.add((grain > 1 ? run : units / ns) * k.weight + over, (k.items * (q + 1) / parts - k.items * q / parts) * ns);
+      }
     }
-    double cost = items <= slots ? longest : std::max(longest, total / slots + 0.5 * longest);
-    if (any) cost += join;
+    const double cost = deal.finish(slots) + (any ? join : 0);
     if (c == top || cost < best_cost) {
       best = c;
       best_cost = cost;
     }
-    if (c <= least) break;
+    if (c <= least || c * slots * 6 < total) break;   // shorter items would only cost more starts
   }
   return best;
 }
@@ -115,18 +197,24 @@ inline void attn_plan(AttnPlan& o, const KvView& c, const KvSeqs& s, int n_heads
     const int64_t packed = int64_t(rows) * group;
     if (packed <= kAttnDecodeMaxRows && !(ride && rows > 0)) {
       const Units u = units_of(len - rows, len - 1, window, sinks, kDecodeUnitShift);
-      dec[nd++] = AttnWork{i, rows, rows == 0 ? 1 : u.count, rows == 0 ? 0 : u.count, 1, 1};
+      dec[nd++] = AttnWork{i, rows, rows == 0 ? 1 : u.count, rows == 0 ? 0 : u.count, 1, 1, 1.0};
       o.decode_rows = std::max(o.decode_rows, int(packed));
     } else {
       const int tiles = int((packed + kPromptRows - 1) / kPromptRows);
       const int last_row = int(int64_t(tiles - 1) * kPromptRows / group), first_end = std::min(rows, (kPromptRows - 1) / group + 1);
       const Units a = units_of(len - rows + last_row, len - 1, window, sinks, kPromptUnitShift);
       const Units b = units_of(len - rows, len - rows + first_end - 1, window, sinks, kPromptUnitShift);
-      pro[np++] = AttnWork{i, rows, std::max(a.count, b.count), std::min(a.count, b.count), tiles, 1};
+      pro[np++] = AttnWork{i, rows, std::max(a.count, b.count), std::min(a.count, b.count), tiles, 1,
+                           packed <= kPromptRows / 2 ? 0.5 : 1.0};
       prompt_items += int64_t(tiles) * c.kv_heads;
     }
   }
   o.decode_tile = o.decode_rows <= 16 ? 16 : 32;
+  auto longer = [](const AttnWork& a, const AttnWork& b) {
+    return a.units_last != b.units_last ? a.units_last > b.units_last : a.index < b.index;
+  };
+  std::sort(dec, dec + nd, longer);
+  std::sort(pro, pro + np, longer);
   // in units: 32 positions' keys and values of a head, against about 64 KiB a block's start costs
   const double unit_bytes = double(c.dim) * elem_bytes * 2 * (1 << kDecodeUnitShift);
   const int dblocks = decode_blocks(c.dim, elem_bytes, o.decode_tile);
@@ -134,8 +222,8 @@ inline void attn_plan(AttnPlan& o, const KvView& c, const KvSeqs& s, int n_heads
                                 kDecodeWaves, kDecodeWaves);
   attn_fill(o.decode, dec, nd, dchunk, s, c.kv_heads, o.decode_tile, group);
   // in units: 64 positions against 256 rows; a split item's sums are 256 fp32 rows written and read
-  const int64_t slots = c.dim == 256 ? kAttnCUs : 2 * kAttnCUs;
-  const int pchunk = prompt_items >= 16 * slots ? 1 << 30 : attn_chunk(pro, np, c.kv_heads, slots, 3, 6, 2, 8, 1);
+  const int64_t slots = c.dim == 64 ? 2 * kAttnCUs : kAttnCUs;
+  const int pchunk = prompt_items >= 16 * slots ? 1 << 30 : attn_chunk(pro, np, c.kv_heads, slots, 1.5, 2, 3, 4, 1);
   attn_fill(o.prompt, pro, np, pchunk, s, c.kv_heads, kPromptRows, group);
 
   size_t rows_o = 0, rows_ml = 0, score = 0;

@@ -10,6 +10,7 @@ namespace {
 // written once.  A block takes kAppendRows consecutive rows, looks their pages
 // up once, and streams their k and v in 16-byte pieces.
 constexpr int kAppendRows = 4;
+constexpr int kAppendDepth = 4;   // pieces a thread has under way
 
 template <typename T>
 __device__ __forceinline__ u32x2 to_e4m3(const u32x4& raw, float scale) {
@@ -47,20 +48,32 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
     base[threadIdx.x] = page_ok(a.c, page) ? page * a.c.page_stride + int64_t(slot) * a.c.token_stride : -1;
   }
   __syncthreads();
-  const int per_head = a.c.dim / 8, per_row = per_head * a.c.kv_heads;
-  for (int u = threadIdx.x; u < 2 * per_row * nr; u += 256) {
-    const bool is_v = u >= per_row * nr;
-    const int w = is_v ? u - per_row * nr : u;
-    const int r = w / per_row, c = w - r * per_row;
-    const int h = c / per_head, e = (c - h * per_head) * 8;
-    if (base[r] < 0) continue;
-    const char* src = (is_v ? a.v : a.k) + (r0 + r) * a.row_stride + h * a.head_stride + e * 2;
-    char* dst = (is_v ? a.c.v : a.c.k) + base[r] + int64_t(h) * a.c.head_stride;
-    const u32x4 x = *reinterpret_cast<const u32x4*>(src);
-    if constexpr (F8)
-      *reinterpret_cast<u32x2*>(dst + e) = to_e4m3<T>(x, (is_v ? a.c.v_scale : a.c.k_scale)[h]);
-    else
-      *reinterpret_cast<u32x4*>(dst + 2 * e) = x;
+  const int per_head = a.c.dim / 8, per_row = per_head * a.c.kv_heads, all = 2 * per_row * nr;
+  for (int u0 = threadIdx.x; u0 < all; u0 += 256 * kAppendDepth) {
+    u32x4 x[kAppendDepth];
+    char* dst[kAppendDepth];
+    float scale[kAppendDepth];
+#pragma unroll
+    for (int n = 0; n < kAppendDepth; ++n) {
+      const int u = min(u0 + n * 256, all - 1);
+      const bool is_v = u >= per_row * nr;
+      const int w = is_v ? u - per_row * nr : u;
+      const int r = w / per_row, c = w - r * per_row;
+      const int h = c / per_head, e = (c - h * per_head) * 8;
+      x[n] = *reinterpret_cast<const u32x4*>((is_v ? a.v : a.k) + (r0 + r) * a.row_stride + int64_t(h) * a.head_stride + e * 2);
+      dst[n] = base[r] < 0 || u0 + n * 256 >= all ? nullptr
+                                                 : (is_v ? a.c.v : a.c.k) + base[r] + int64_t(h) * a.c.head_stride +
+                                                       e * (F8 ? 1 : 2);
+      if constexpr (F8) scale[n] = (is_v ? a.c.v_scale : a.c.k_scale)[h];
+    }
+#pragma unroll
+    for (int n = 0; n < kAppendDepth; ++n) {
+      if (!dst[n]) continue;
+      if constexpr (F8)
+        *reinterpret_cast<u32x2*>(dst[n]) = to_e4m3<T>(x[n], scale[n]);
+      else
+        *reinterpret_cast<u32x4*>(dst[n]) = x[n];
+    }
   }
 }
 
