@@ -19,18 +19,6 @@ constexpr int kBN = 1 << kPromptUnitShift;
 constexpr int kWaves = 8;   // 32 packed rows each; four bring keys, four values
 constexpr int kAhead = 4;   // fragments read ahead of the products
 
-// Order of a run of STEPS products (PER MFMAs each) whose fragments take READS LDS reads.
-template <int AHEAD, int STEPS, int PER, int READS>
-__device__ __forceinline__ void sched_pipeline() {
-  constexpr int kMfma = 0x8, kRead = 0x100;
-  __builtin_amdgcn_sched_group_barrier(kRead, (AHEAD < STEPS ? AHEAD : STEPS) * READS, 0);
-#pragma unroll
-  for (int k = 0; k < STEPS; ++k) {
-    __builtin_amdgcn_sched_group_barrier(kMfma, PER, 0);
-    if (k + AHEAD < STEPS) __builtin_amdgcn_sched_group_barrier(kRead, READS, 0);
-  }
-}
-
 // Values of a fragment: lane's column d = db * 32 + (lane & 31), eight positions of
 // 16-position step st in the order of the weights' registers.
 template <typename T, bool F8, int DIM>

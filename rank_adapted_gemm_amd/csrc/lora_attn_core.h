@@ -75,6 +75,18 @@ __device__ __forceinline__ float max_rows16(float x) {   // over lanes l and l ^
   return __builtin_fmaxf(__builtin_bit_cast(float, uint32_t(r[0])), __builtin_bit_cast(float, uint32_t(r[1])));
 }
 
+// Order of a run of STEPS products (PER MFMAs each) whose fragments take READS LDS reads.
+template <int AHEAD, int STEPS, int PER, int READS>
+__device__ __forceinline__ void sched_pipeline() {
+  constexpr int kMfma = 0x8, kRead = 0x100;
+  __builtin_amdgcn_sched_group_barrier(kRead, (AHEAD < STEPS ? AHEAD : STEPS) * READS, 0);
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) {
+    __builtin_amdgcn_sched_group_barrier(kMfma, PER, 0);
+    if (k + AHEAD < STEPS) __builtin_amdgcn_sched_group_barrier(kRead, READS, 0);
+  }
+}
+
 // Exponent bits of a 16-bit type: all ones in infinities and NaN.
 template <typename T>
 constexpr uint32_t kExpBits = __is_same(T, __bf16) ? 0x7F80u : 0x7C00u;

@@ -1,27 +1,37 @@
 // Weight that each cached position received from a prompt's rows.
 //
 // The rows' totals are only known after their attention, so the scores are
-// computed again: a block keeps 128 positions of one key-value head in registers
-// (32 a wave, as the first operand of the product) and walks the packed rows
-// that see any of them 64 at a time through LDS.  Half of attention's products;
-// the exponential of every score is the other bound.  Sums stay in one block, so
+// computed again: half of attention's products, and the exponential of every
+// score beside them.  A block takes 64 positions of one key-value head and walks
+// the packed rows that see any of them; its four waves hold 32 positions each in
+// registers, as the first operand of the product, and two of them share a half of
+// the rows of a step, which DMA loads bring to LDS one step ahead.  Early
+// positions are seen by every row, so a block's length is what a launch can last:
+// 64 positions keep it at half of what 128 would.  Sums stay in one block, so
 // their order depends on the shapes alone.
 #include "lora_attn_core.h"
 
 namespace lora {
 namespace {
 
-constexpr int kQN = 64;   // packed rows of a step
+constexpr int kWaves = 4;
+
+// Global -> LDS by 64-bit addresses, as dma16.
+__device__ __forceinline__ void dma16_from(const char* p, uint32_t lds_addr) {
+  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(p),
+               "s"(__builtin_amdgcn_readfirstlane(lds_addr)) : "memory");
+}
 
 template <typename T, bool F8, int DIM>
-__global__ __launch_bounds__(256, DIM == 64 ? 4 : 2) void prompt_mass_kernel(AttnArgs a, AttnPart part) {
+__global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_mass_kernel(AttnArgs a, AttnPart part) {
   using Q = Row<false, DIM>;   // rows of q are 16 bits wide whatever the cache holds
   using x8 = typename Vec<T>::x8;
-  constexpr int KS = DIM / 16, TILE = kQN * Q::kBytes, NX = TILE / 16 / 256;   // 16-byte pieces of a step a thread
+  constexpr int KS = DIM / 16, QN = DIM == 256 ? 64 : 128, QW = QN / 2;   // rows of a step, of a wave in it
+  constexpr int TILE = QN * Q::kBytes, LOADS = TILE / 1024 / kWaves;
+  constexpr int AHEAD = 4;
   __shared__ __attribute__((aligned(1024))) char lds[2 * TILE];
-  __shared__ float lse[2][kQN];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int hh = lane >> 5, col = lane & 31;
+  const int hh = lane >> 5, col = lane & 31, qg = wave >> 1;
   const int s = seq_of_item(part, blockIdx.x);
   const AttnSeq sq = part.seq[s];
   const int r = int(blockIdx.x) - (s == 0 ? 0 : part.seq[s - 1].item_end);
@@ -33,7 +43,7 @@ __global__ __launch_bounds__(256, DIM == 64 ? 4 : 2) void prompt_mass_kernel(Att
   const int j1 = a.window < 0 || b0 < a.sinks ? sq.rows
                                               : int(min(int64_t(sq.rows), max(int64_t(0), int64_t(b1) - 1 + a.window - t0)));
   const int m0 = j0 * a.group, m1 = j1 * a.group;
-  const int p0 = b0 + wave * 32, p = p0 + col;
+  const int p0 = b0 + (wave & 1) * 32, p = p0 + col;
   const Pages pages = pages_of(a, sq.index, t0, sq.kv_len - 1);
 
   // keys: lane's position, 8 of its dimensions a product
@@ -63,62 +73,91 @@ __global__ __launch_bounds__(256, DIM == 64 ? 4 : 2) void prompt_mass_kernel(Att
     }
   }
   const bool anybad = __any(bad);
-  const float c = a.scale * kLog2e * (F8 ? a.c.k_scale[head] : 1.0f);
+  const float c = uniform(a.scale * kLog2e * (F8 ? a.c.k_scale[head] : 1.0f));
 
-  u32x4 next[NX];
-  float next_lse = INFINITY;
-  auto fetch = [&](int m) {
+  // A step's first packed row m is row j and head h of the group; the n-th after it lies over(h + n) rows on.
+  const uint32_t group = a.group, magic = uint32_t(((uint64_t(1) << 32) + group - 1) / group);
+  auto over = [&](uint32_t x) { return group == 1 ? x : __umulhi(x, magic); };   // x / group, x < 2^16
+  const uint32_t lds0 = lds_addr(lds);
+  const int lrow = lane / Q::kChunks, lslot = lane % Q::kChunks;
+  constexpr int RPL = Q::kRowsPerLoad;
+  uint32_t j = uint32_t(j0), h = 0;
+  auto advance = [&] {
+    h += QN;
+    const uint32_t dj = over(h);
+    j += dj;
+    h -= dj * group;
+  };
+  auto issue = [&](int m, int buf) {
 #pragma unroll
-    for (int x = 0; x < NX; ++x) {
-      const int at = x * 256 + tid, row = at / Q::kChunks, ch = at - row * Q::kChunks;
-      const int mr = min(m + row, m1 - 1), j = mr / a.group, h = mr - j * a.group + head * a.group;
-      next[x] = *reinterpret_cast<const u32x4*>(a.q + (sq.q_start + j) * a.q_row_stride + int64_t(h) * a.q_head_stride + ch * 16);
-    }
-    if (tid < kQN) {
-      const int mr = m + tid, j = min(mr, m1 - 1) / a.group;
-      const float v = a.lse[int64_t(sq.q_start + j) * a.heads + (min(mr, m1 - 1) - j * a.group) + head * a.group];
-      next_lse = mr < m1 && v != -INFINITY ? v : INFINITY;   // a row that sees nothing gives no weight
+    for (int x = 0; x < LOADS; ++x) {
+      const int row = (wave * LOADS + x) * RPL + lrow;
+      const uint32_t n = h + uint32_t(min(row, m1 - 1 - m)), dj = over(n);
+      const char* src = a.q + int64_t(sq.q_start + int(j + dj)) * a.q_row_stride +
+                        int64_t(int(n - dj * group) + head * int(group)) * a.q_head_stride +
+                        ((lslot ^ Q::key_swizzle(row)) << 4);
+      dma16_from(src, lds0 + buf * TILE + (wave * LOADS + x) * 1024);
     }
   };
-  auto store = [&](int buf) {
-#pragma unroll
-    for (int x = 0; x < NX; ++x) {
-      const int at = x * 256 + tid, row = at / Q::kChunks, ch = at - row * Q::kChunks;
-      *reinterpret_cast<u32x4*>(lds + buf * TILE + row * Q::kBytes + ((ch ^ Q::key_swizzle(row)) << 4)) = next[x];
-    }
-    if (tid < kQN) lse[buf][tid] = next_lse;
+  // the wave's rows' totals: of row qg * QW + lane of the step
+  auto total = [&](int m) {
+    const int row = qg * QW + (lane & (QW - 1));
+    const uint32_t n = h + uint32_t(min(row, m1 - 1 - m)), dj = over(n);
+    const float v = a.lse[int64_t(sq.q_start + int(j + dj)) * a.heads + int(n - dj * group) + head * int(group)];
+    return m + row < m1 && v != -INFINITY ? v : INFINITY;   // a row that sees nothing gives no weight
   };
 
   f32x16 acc;
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0;
-  const uint32_t qbase = uint32_t(col * Q::kBytes + ((hh ^ Q::key_swizzle(col)) << 4));
+  const uint32_t qbase = uint32_t((qg * QW + col) * Q::kBytes + ((hh ^ Q::key_swizzle(col)) << 4));
+  float next = INFINITY;
   if (m0 < m1) {
-    fetch(m0);
-    store(0);
+    issue(m0, 0);
+    next = total(m0);
   }
-  __syncthreads();
-  for (int m = m0, buf = 0; m < m1; m += kQN, buf ^= 1) {
-    if (m + kQN < m1) fetch(m + kQN);
+  for (int m = m0, buf = 0; m < m1; m += QN, buf ^= 1) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" : "+v"(next) : : "memory");
+    const uint32_t lu = __builtin_bit_cast(uint32_t, next);
+    const int tj = t0 + int(j);
+    const uint32_t th = h;
+    auto time_of = [&](int n) { return tj + int(over(th + uint32_t(min(n, m1 - 1 - m)))); };   // position of row m + n
+    if (m + QN < m1) {
+      advance();
+      issue(m + QN, buf ^ 1);
+      next = total(m + QN);
+    }
+    const auto both = __builtin_amdgcn_permlane32_swap(lu, lu, false, false);   // rows 0 - 31 and 32 - 63 to either half
 #pragma unroll
-    for (int half = 0; half < kQN / 32; ++half) {
-      const int ma = m + half * 32;
+    for (int half = 0; half < QW / 32; ++half) {
+      const int na = qg * QW + half * 32, ma = m + na;
       if (ma >= m1) continue;
-      const int ta = t0 + ma / a.group, tb = t0 + min(ma + 31, m1 - 1) / a.group;
+      const int ta = time_of(na), tb = time_of(na + 31);
       if (p0 > tb || p0 >= b1) continue;
       f32x16 st;
 #pragma unroll
       for (int e = 0; e < 16; ++e) st[e] = 0;
+      const uint32_t qa = lds0 + buf * TILE + half * 32 * Q::kBytes + qbase;
+      auto nth = [](int n) { return KS > 8 ? (n >> 1) | (n & 1) << 3 : n; };
+      auto read = [&](int n) {
+        typedef __attribute__((address_space(3))) const u32x4* kp;
+        return *kp(uintptr_t((qa ^ uint32_t((nth(n) & 7) * 32)) + (nth(n) >> 3) * 256));
+      };
+      u32x4 f[AHEAD];
+#pragma unroll
+      for (int x = 0; x < AHEAD; ++x) f[x] = read(x);
 #pragma unroll
       for (int x = 0; x < KS; ++x) {
-        const x8 q = *reinterpret_cast<const x8*>(lds + buf * TILE + half * 32 * Q::kBytes + (qbase ^ uint32_t(x * 32)));
-        st = mfma32<T>(k[x], q, st);
+        const x8 q = __builtin_bit_cast(x8, f[x % AHEAD]);
+        if (x + AHEAD < KS) f[x % AHEAD] = read(x + AHEAD);
+        st = mfma32<T>(k[nth(x)], q, st);
       }
-      const float l = lse[buf][half * 32 + col];
+      sched_pipeline<AHEAD, KS, 1, 1>();
+      const float l = __builtin_bit_cast(float, half == 0 ? uint32_t(both[0]) : uint32_t(both[1]));
       const bool masked = anybad || !(p0 + 31 <= ta && p0 + 31 < b1 &&
                                       (a.window < 0 || p0 >= tb - a.window + 1 || p0 + 31 < a.sinks));
       if (masked) {
-        const int t = t0 + min(ma + col, m1 - 1) / a.group;
+        const int t = time_of(na + col);
         const int low = a.window < 0 ? 0 : t - a.window + 1;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -133,20 +172,24 @@ __global__ __launch_bounds__(256, DIM == 64 ? 4 : 2) void prompt_mass_kernel(Att
         for (int e = 0; e < 16; ++e) acc[e] += __builtin_amdgcn_exp2f(__builtin_fmaf(st[e], c, -l));
       }
     }
-    if (m + kQN < m1) store(buf ^ 1);
-    __syncthreads();
   }
-  // over the rows' lanes
+  // over the rows' lanes, then over the two waves that share positions
+  float mine = 0;   // the lane's position: p0 + place, for the first 16 lanes of either half
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     float x = acc[e];
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) x += __shfl_xor(x, d);
-    const int pe = p0 + (e >> 2) * 8 + hh * 4 + (e & 3);
-    if (col == e && pe < b1) {
-      const int64_t at = (int64_t(sq.index) * a.c.kv_heads + head) * a.mass_cap + pe;
-      a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.0f) + x;
-    }
+    mine = col == e ? x : mine;
+  }
+  __syncthreads();   // every wave is past its last read of the ring
+  float* other = reinterpret_cast<float*>(lds);
+  const int place = (col >> 2) * 8 + hh * 4 + (col & 3);
+  if (qg == 1 && col < 16) other[(wave & 1) * 32 + place] = mine;
+  __syncthreads();
+  if (qg == 0 && col < 16 && p0 + place < b1) {
+    const int64_t at = (int64_t(sq.index) * a.c.kv_heads + head) * a.mass_cap + p0 + place;
+    a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.0f) + (mine + other[(wave & 1) * 32 + place]);
   }
 }
 

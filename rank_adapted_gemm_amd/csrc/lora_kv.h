@@ -158,7 +158,7 @@ constexpr int kAttnDecodeRows = 16;       // packed rows a decode tile holds for
 constexpr int kAttnDecodeMaxRows = 32;    // sequences of at most that many packed rows are decoded
 constexpr int kDecodeWaves = 4;
 constexpr int kPromptRows = 256;      // packed rows of a prompt tile
-constexpr int kMassRows = 128;        // positions of a prompt's weight block
+constexpr int kMassRows = 64;         // positions of a prompt's weight block
 
 // LDS of a decode wave: a ring of 16 KiB, or of one step's keys and values where those take 32, and at the
 // end its fp32 outputs, padded against bank conflicts.
