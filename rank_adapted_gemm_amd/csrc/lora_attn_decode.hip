@@ -62,6 +62,67 @@ struct ValueReader16 {
   }
 };
 
+// Joins a row's items without a launch of its own: an item that is done says so in the workspace, and one
+// that then finds all of its row's items done adds them up.  `arrived` needs no initial value: it holds the
+// number of the call, which no other call has, and is cleared by the join, so that the same launch may run
+// again from a graph.  Two items may both find the row complete; they write the same values.  Sums and
+// marks go past the XCD's L2 (device scope): the other items run on other XCDs.
+template <typename T, int DIM>
+__device__ __forceinline__ void join_last(const AttnArgs& a, const AttnSeq& sq, int first, int head, int tile_rows, int M,
+                                          float vs, float* lds) {
+  const int tid = threadIdx.x;
+  uint64_t* arrived = a.arrived + first + head;   // of the row's first split; the others a head count apart
+  const int64_t slot0 = (int64_t(first) + head) * tile_rows, step = int64_t(a.c.kv_heads) * tile_rows;
+  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+  __syncthreads();                                // every thread's sums are where the others will look
+  if (tid == 0)
+    __hip_atomic_exchange(a.arrived + blockIdx.x, a.call, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+  __syncthreads();
+  bool missing = false;
+  for (int i = tid; i < sq.nsplit; i += kWaves * 64)
+    missing |= __hip_atomic_load(arrived + int64_t(i) * a.c.kv_heads, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != a.call;
+  if (__syncthreads_or(missing)) return;
+  const uint32_t span = uint32_t((sq.nsplit - 1) * step + tile_rows);
+  const auto po = make_rsrc(a.part_o + slot0 * DIM, span * DIM * 4), pm = make_rsrc(a.part_ml + slot0 * 2, span * 8);
+  // maxima and sums of all rows and splits
+  float* ml = lds;
+  for (int z = tid; z < M * sq.nsplit; z += kWaves * 64) {
+    const int m = z / sq.nsplit, i = z - m * sq.nsplit;
+    const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(pm, uint32_t(m + i * step) * 8, 0, kDeviceScope);
+    *reinterpret_cast<u32x2*>(ml + 2 * z) = x;
+  }
+  __syncthreads();
+  for (int z = tid; z < M * (DIM / 4); z += kWaves * 64) {
+    const int m = z / (DIM / 4), d = (z - m * (DIM / 4)) * 4;
+    const float* mine = ml + 2 * m * sq.nsplit;
+    float top = kLowest, total = 0;
+    for (int i = 0; i < sq.nsplit; ++i) top = __builtin_fmaxf(top, mine[2 * i]);
+    f32x4 acc = {0, 0, 0, 0};
+    for (int i0 = 0; i0 < sq.nsplit; i0 += 8) {
+      f32x4 o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        o[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                             po, (uint32_t(m + min(i0 + i, sq.nsplit - 1) * step) * DIM + d) * 4, 0, kDeviceScope));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i0 + i >= sq.nsplit) continue;
+        const float f = __builtin_amdgcn_exp2f(mine[2 * (i0 + i)] - top);
+        total += mine[2 * (i0 + i) + 1] * f;
+        acc += o[i] * f;
+      }
+    }
+    const float inv = total == 0 ? 0.0f : vs / total;
+    const int j = m / a.group;
+    const int64_t row = int64_t(sq.q_start + j) * a.heads + (m - j * a.group) + head * a.group;
+    *reinterpret_cast<u32x2*>(a.out + (row * DIM + d) * 2) =
+        u32x2{pack_pair<T>(acc[0] * inv, acc[1] * inv), pack_pair<T>(acc[2] * inv, acc[3] * inv)};
+  }
+  for (int i = tid; i < sq.nsplit; i += kWaves * 64)
+    __hip_atomic_store(arrived + int64_t(i) * a.c.kv_heads, uint64_t(0), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // QT: 16-row columns of packed rows.  MASS: scores go to the workspace.
 template <typename T, bool F8, int DIM, int QT, bool MASS>
 __global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16)) void decode_kernel(AttnArgs a, AttnPart part) {
@@ -289,6 +350,11 @@ __global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16
       slow_row<T, F8, DIM>(a, sq, pages, units, u0, nu, kStep, t0, item.head, m,
                            sq.nsplit > 1 ? int64_t(blockIdx.x) * BM + m : -1,
                            sq.nsplit > 1 || MASS ? int64_t(blockIdx.x) * BM + m : -1);
+    if constexpr (!MASS) {
+      __threadfence();   // rows of slow_row lie in this XCD's L2
+      if (a.arrived && sq.nsplit > 1)
+        join_last<T, DIM>(a, sq, first, item.head, BM, M, F8 ? a.c.v_scale[item.head] : 1.0f, reinterpret_cast<float*>(lds));
+    }
     return;
   }
   // the waves' rows meet in LDS
@@ -310,6 +376,8 @@ __global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16
   }
   __syncthreads();
   const float vs = F8 ? a.c.v_scale[item.head] : 1.0f;
+  const auto po = make_rsrc(a.part_o + int64_t(blockIdx.x) * BM * DIM, BM * DIM * 4);
+  const auto pm = make_rsrc(a.part_ml + int64_t(blockIdx.x) * BM * 2, BM * 8);
   for (int z = tid; z < M * (DIM / 4); z += kWaves * 64) {
     const int m = z / (DIM / 4), d = (z - m * (DIM / 4)) * 4;
     float best = ml[0][m][0];
@@ -324,9 +392,10 @@ __global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16
       acc += *reinterpret_cast<const f32x4*>(lds + y * WAVE_LDS + (m * (DIM + 4) + d) * 4) * f;
     }
     if (sq.nsplit > 1) {
-      const int64_t slot = int64_t(blockIdx.x) * BM + m;
-      *reinterpret_cast<f32x4*>(a.part_o + slot * DIM + d) = acc;
-      if (d == 0) *reinterpret_cast<f32x2*>(a.part_ml + slot * 2) = f32x2{best, total};
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc), po, uint32_t(m * DIM + d) * 4, 0, kDeviceScope);
+      if (d == 0)
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, f32x2{best, total}), pm, uint32_t(m) * 8, 0,
+                                              kDeviceScope);
     } else {
       const float inv = total == 0 ? 0.0f : vs / total;
       const int j = m / a.group;
@@ -336,6 +405,9 @@ __global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16
       // accumulated weights are taken against these, also where the rows were not split
       if (MASS && d == 0) *reinterpret_cast<f32x2*>(a.part_ml + (int64_t(blockIdx.x) * BM + m) * 2) = f32x2{best, total};
     }
+  }
+  if constexpr (!MASS) {
+    if (a.arrived && sq.nsplit > 1) join_last<T, DIM>(a, sq, first, item.head, BM, M, vs, reinterpret_cast<float*>(lds));
   }
 }
 

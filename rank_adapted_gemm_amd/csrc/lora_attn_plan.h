@@ -22,7 +22,8 @@ struct AttnPlan {
   AttnPath decode, prompt;
   int decode_rows;             // packed rows of the tallest decoded sequence
   int decode_tile;             // rows of a decode tile: 16 or 32
-  size_t off_lse, off_ml, off_scores, off_o, bytes;
+  bool inside[kAttnParts];     // the last item of a row joins it, without a launch
+  size_t off_lse, off_ml, off_scores, off_arrived, off_o, bytes;
 };
 
 // A sequence's work for one kernel.
@@ -215,22 +216,27 @@ inline void attn_plan(AttnPlan& o, const KvView& c, const KvSeqs& s, int n_heads
   };
   std::sort(dec, dec + nd, longer);
   std::sort(pro, pro + np, longer);
-  // in units: 32 positions' keys and values of a head, against about 64 KiB a block's start costs
+  // In units of 32 positions' keys and values of a head: a block's start costs what a CU streams meanwhile,
+  // less where a second block streams beside it, and leaving sums their bytes twice.
   const double unit_bytes = double(c.dim) * elem_bytes * 2 * (1 << kDecodeUnitShift);
   const int dblocks = decode_blocks(c.dim, elem_bytes, o.decode_tile);
-  const int dchunk = attn_chunk(dec, nd, c.kv_heads, dblocks * kAttnCUs, 65536 / unit_bytes, 0, 98304 / unit_bytes,
-                                kDecodeWaves, kDecodeWaves);
+  const int dchunk = attn_chunk(dec, nd, c.kv_heads, dblocks * kAttnCUs, (dblocks == 2 ? 32768 : 98304) / unit_bytes,
+                                o.decode_rows * c.dim * 8 / unit_bytes, 98304 / unit_bytes, kDecodeWaves, kDecodeWaves);
   attn_fill(o.decode, dec, nd, dchunk, s, c.kv_heads, o.decode_tile, group);
   // in units: 64 positions against 256 rows; a split item's sums are 256 fp32 rows written and read
   const int64_t slots = c.dim == 64 ? 2 * kAttnCUs : kAttnCUs;
   const int pchunk = prompt_items >= 16 * slots ? 1 << 30 : attn_chunk(pro, np, c.kv_heads, slots, 1.5, 2, 3, 4, 1);
   attn_fill(o.prompt, pro, np, pchunk, s, c.kv_heads, kPromptRows, group);
 
-  size_t rows_o = 0, rows_ml = 0, score = 0;
+  size_t rows_o = 0, rows_ml = 0, score = 0, arrived = 0;
   for (int i = 0; i < o.decode.parts; ++i) {
     const AttnPart& p = o.decode.part[i];
     rows_o = std::max(rows_o, size_t(p.split_items) * o.decode_tile);
     rows_ml = std::max(rows_ml, size_t(mass ? p.items : p.split_items) * o.decode_tile);
+    o.inside[i] = !mass;
+    for (int k = 0; k < p.n; ++k)
+      if (int64_t(p.seq[k].rows) * group * p.seq[k].nsplit * c.dim * 4 > kJoinInside) o.inside[i] = false;
+    if (o.inside[i]) arrived = std::max(arrived, size_t(p.split_items) * 8);
     if (mass) score = std::max(score, size_t(p.items) * o.decode_rows * p.score_cols * 4);
   }
   for (int i = 0; i < o.prompt.parts; ++i) {
@@ -242,7 +248,8 @@ inline void attn_plan(AttnPlan& o, const KvView& c, const KvSeqs& s, int n_heads
   o.off_lse = 0;
   o.off_ml = mass && np > 0 ? up(size_t(s.q_start[s.n]) * n_heads * 4) : 0;
   o.off_scores = o.off_ml + up(rows_ml * 8);
-  o.off_o = o.off_scores + up(score);
+  o.off_arrived = o.off_scores + up(score);
+  o.off_o = o.off_arrived + up(arrived);
   o.bytes = o.off_o + up(rows_o * c.dim * 4);
 }
 

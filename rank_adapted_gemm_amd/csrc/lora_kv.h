@@ -142,6 +142,8 @@ struct AttnArgs {
   float* part_o;         // workspace: unnormalised output rows of split items
   float* part_ml;        // workspace: their maximum and sum
   float* scores;         // workspace: scaled scores of decode items (accumulated weights), or NULL
+  uint64_t* arrived;     // workspace: decode items that are done, or NULL where a launch of its own joins them
+  uint64_t call;         // this call's number, which `arrived` holds for them
   int64_t q_row_stride;  // bytes
   int64_t mass_cap;
   int32_t q_head_stride; // bytes
@@ -158,6 +160,7 @@ constexpr int kAttnDecodeRows = 16;       // packed rows a decode tile holds for
 constexpr int kAttnDecodeMaxRows = 32;    // sequences of at most that many packed rows are decoded
 constexpr int kDecodeWaves = 4;
 constexpr int kPromptRows = 256;      // packed rows of a prompt tile
+constexpr int kJoinInside = 256 * 1024;   // bytes of sums that the last decode item of a row joins itself
 constexpr int kMassRows = 64;         // positions of a prompt's weight block
 
 // LDS of a decode wave: a ring of 16 KiB, or of one step's keys and values where those take 32, and at the

@@ -97,7 +97,7 @@ constexpr int kSelWaves = kSelThreads / 64;
 constexpr uint32_t kStays = 0xFFFFFFFFu;
 
 // Finds the bin, counting from the highest of n (2 a thread), where `k` keys are reached;
-// sel[0] = the bin, sel[1] = how many of its keys are among the k.  The histogram is `copies` long ones.
+// sel[0] = the bin, sel[1] = how many of its keys are among the k.  A bin's `copies` counts lie side by side.
 __device__ __forceinline__ void select_bin(const uint32_t* hist, int n, int copies, uint32_t k, uint32_t* wave_sum,
                                            uint32_t* sel) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -105,8 +105,8 @@ __device__ __forceinline__ void select_bin(const uint32_t* hist, int n, int copi
   uint32_t c0 = 0, c1 = 0;
   if (b > 0)
     for (int x = 0; x < copies; ++x) {
-      c0 += hist[x * n + b];
-      c1 += hist[x * n + b - 1];
+      c0 += hist[b * copies + x];
+      c1 += hist[(b - 1) * copies + x];
     }
   uint32_t upto = c0 + c1;
 #pragma unroll
@@ -139,8 +139,8 @@ __device__ __forceinline__ void keep_all(const EvictArgs& a, int len, const floa
 // Keys stay in registers, four consecutive positions a thread in each of G groups of 4,096: the weights
 // are read once.  Few pairs leave most CUs idle, so what counts is the instructions a key costs: about
 // 512 cycles each at G = 8.  Digits of 11, 11 and 10 bits: with the sign, the exponent and two bits of
-// the mantissa in the first, weights of usual spread fall on enough bins, and four copies of the
-// histogram keep lanes with equal weights (zeros above all) apart.
+// the mantissa in the first, weights of usual spread fall on enough bins, and four copies of each
+// keep lanes with equal weights (zeros above all) apart, in banks of their own.
 template <int G>
 __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(EvictArgs a) {
   constexpr int kCopies = 4;
@@ -185,14 +185,14 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(EvictArgs a) 
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11, copies = pass == 0 ? kCopies : 1;
     for (int x = tid; x < copies << bits; x += kSelThreads) hist[x] = 0;
     __syncthreads();
-    uint32_t* mine = hist + (pass == 0 ? (lane & (kCopies - 1)) << bits : 0);
+    uint32_t* mine = hist + (pass == 0 ? lane & (kCopies - 1) : 0);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       if (g * 4 * kSelThreads >= len) continue;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (pass == 0 || key[g][e] >> (shift + bits) == prefix)
-          atomicAdd(&mine[(key[g][e] >> shift) & ((1u << bits) - 1)], 1u);
+          atomicAdd(&mine[((key[g][e] >> shift) & ((1u << bits) - 1)) * copies], 1u);
     }
     __syncthreads();
     select_bin(hist, 1 << bits, copies, k, wave_sum, sel);

@@ -2,6 +2,8 @@
 #include <string.h>
 
 #include <algorithm>
+#include <atomic>
+#include <chrono>
 
 #include "lora_attn_plan.h"
 #include "lora_kv.h"
@@ -100,6 +102,14 @@ size_t span_bytes(int64_t rows, int64_t row_stride, int64_t heads, int64_t head_
 
 bool hits_cache(const void* p, size_t n, const KvView& c, size_t pool_bytes) {
   return overlaps(p, n, c.k, pool_bytes) || overlaps(p, n, c.v, pool_bytes);
+}
+
+// A number that no other launch of this process has and that a workspace's earlier contents do not hold by
+// accident: a counter, spread over 64 bits.
+uint64_t call_number() {
+  static std::atomic<uint64_t> next{uint64_t(std::chrono::steady_clock::now().time_since_epoch().count()) | 1};
+  const uint64_t x = next.fetch_add(2, std::memory_order_relaxed) * 0x9E3779B97F4A7C15u;
+  return x;   // odd times odd: never 0, which marks an item that is not done
 }
 
 lora_status check_heads(const KvView& c, const KvSeqs& s, int32_t n_heads) {
@@ -216,6 +226,8 @@ lora_status lora_attn(const lora_kv_cache* cache, const lora_kv_batch* batch,
   a.table = batch->page_table;
   a.table_stride = batch->table_stride;
   a.lse = nullptr;
+  a.arrived = nullptr;
+  a.call = 0;
   a.part_ml = reinterpret_cast<float*>(ws + plan.off_ml);
   a.part_o = reinterpret_cast<float*>(ws + plan.off_o);
   a.scores = mass_out ? reinterpret_cast<float*>(ws + plan.off_scores) : nullptr;
@@ -232,10 +244,13 @@ lora_status lora_attn(const lora_kv_cache* cache, const lora_kv_batch* batch,
   hipError_t e = hipSuccess;
   for (int i = 0; i < plan.decode.parts && e == hipSuccess; ++i) {
     const lora::AttnPart& p = plan.decode.part[i];
+    const bool inside = plan.inside[i] && p.split_items > 0;
+    a.arrived = inside ? reinterpret_cast<uint64_t*>(ws + plan.off_arrived) : nullptr;
+    a.call = inside ? call_number() : 0;
     if (p.items > 0) e = lora::launch_attn_decode(a, p, plan.decode_rows, dtype, cache->dtype, stream);
     if (e == hipSuccess && mass_out)
       e = lora::launch_attn_decode_finish(a, p, plan.decode_tile, plan.decode_rows, dtype, stream);
-    else if (e == hipSuccess && p.split_items > 0)
+    else if (e == hipSuccess && p.split_items > 0 && !inside)
       e = lora::launch_attn_join(a, p, plan.decode_tile, plan.decode.join_rows[i], dtype, stream);
   }
   a.lse = mass_out ? reinterpret_cast<float*>(ws + plan.off_lse) : nullptr;
