@@ -163,13 +163,12 @@ __global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16
     for (int g = 0; g < 2; ++g) pv[g] = n < mine ? pages.page(a.c, p0 + g * 16) : -2;
   };
   auto issue = [&](int i, bool values) {
-    // past the end: loads that bring zeros, so that every wait counts the same
-    const int p0 = i < mine ? units.unit(u0 + wave + i * kWaves) * kStep : 0;
+    const int p0 = units.unit(u0 + wave + i * kWaves) * kStep;
     const uint32_t dst = ring + uint32_t((i & (NS - 1)) * 2 + (values ? 1 : 0)) * STEP;
     constexpr int G = R::kLoads < 4 ? R::kLoads : 4;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const int page = i < mine ? __builtin_amdgcn_readlane(pv[g], i & 63) : -2;
+      const int page = __builtin_amdgcn_readlane(pv[g], i & 63);
       const uint32_t bit = 1u << (2 * (i & (NS - 1)) + g);
       if (!values) ringbad = page == -1 ? ringbad | bit : ringbad & ~bit;
       const i32x4 rs = group_rsrc(a.c, values ? a.c.v : a.c.k, page, p0 + g * 16, item.head, R::kBytes);
@@ -214,6 +213,7 @@ __global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16
   asm volatile("s_waitcnt vmcnt(0)" : "+v"(pv[0]), "+v"(pv[1]) : : "memory");
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
+    if (i >= mine) continue;
     issue(i, false);
     issue(i, true);
   }
@@ -237,7 +237,9 @@ __global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16
     const int p0 = units.unit(u0 + wave + i * kWaves) * kStep;
     const uint32_t kt = ring + uint32_t((i & (NS - 1)) * 2) * STEP, vt = kt + STEP;
     const uint32_t badp = (ringbad >> (2 * (i & (NS - 1)))) & 3u;
-    wait_vm<(2 * NS - 1) * NL>();   // all but what was issued after this step's keys
+    const bool more = i + NS < mine;   // the ring is full: a count tells what was issued after a step's loads
+    if (more) wait_vm<(2 * NS - 1) * NL>();
+    else wait_vm<NL>();
     typedef __attribute__((address_space(3))) const u32x4* kp;
     f32x4 st[QT][2];
 #pragma unroll
@@ -264,9 +266,11 @@ __global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16
         }
       }
     }
-    if (((i + NS) & 63) == 0) load_pages(i + NS);
-    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");   // the keys are in registers: their place may be filled
-    issue(i + NS, false);
+    if (more) {
+      if (((i + NS) & 63) == 0) load_pages(i + NS);
+      asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");   // the keys are in registers: their place may be filled
+      issue(i + NS, false);
+    }
 
     const bool masked = badp != 0 ||
                         !(p0 + kStep - 1 <= t_lo && (a.window < 0 || p0 >= lowx || p0 + kStep - 1 < a.sinks));
@@ -317,7 +321,8 @@ __global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16
       }
       w[x] = __builtin_bit_cast(x8, pk);
     }
-    wait_vm<(2 * NS - 1) * NL>();
+    if (more) wait_vm<(2 * NS - 1) * NL>();
+    else wait_vm<0>();
     if (masked) {
       // a hidden position may hold anything: infinities and NaN leave the values, and a row that sees one
       // is gone over again
@@ -340,8 +345,10 @@ __global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16
 #pragma unroll
       for (int x = 0; x < QT; ++x) o[x][d] = mfma16<T>(vf, w[x], o[x][d]);
     }
-    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
-    issue(i + NS, true);
+    if (more) {
+      asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+      issue(i + NS, true);
+    }
   }
 
   wait_vm<0>();

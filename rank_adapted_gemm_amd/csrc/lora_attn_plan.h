@@ -221,7 +221,7 @@ inline void attn_plan(AttnPlan& o, const KvView& c, const KvSeqs& s, int n_heads
   const double unit_bytes = double(c.dim) * elem_bytes * 2 * (1 << kDecodeUnitShift);
   const int dblocks = decode_blocks(c.dim, elem_bytes, o.decode_tile);
   const int dchunk = attn_chunk(dec, nd, c.kv_heads, dblocks * kAttnCUs, (dblocks == 2 ? 32768 : 98304) / unit_bytes,
-                                o.decode_rows * c.dim * 8 / unit_bytes, 98304 / unit_bytes, kDecodeWaves, kDecodeWaves);
+                                o.decode_rows * c.dim * 8 / unit_bytes, 98304 / unit_bytes, 2, 1);
   attn_fill(o.decode, dec, nd, dchunk, s, c.kv_heads, o.decode_tile, group);
   // in units: 64 positions against 256 rows; a split item's sums are 256 fp32 rows written and read
   const int64_t slots = c.dim == 64 ? 2 * kAttnCUs : kAttnCUs;
