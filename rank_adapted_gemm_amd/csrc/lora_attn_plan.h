@@ -93,10 +93,10 @@ struct AttnDeal {
 };
 
 // The longest run of units an item may take, so that the launch ends soonest.  `each` and `split` are what
-// an item and what leaving sums in the workspace cost in units, `join` the join's launch; an item's waves
-// take `grain` units at a time.
+// an item and what leaving sums in the workspace cost in units, `join` the join's launch.  `shared`: what a
+// unit costs where two items share a slot, 0 where they cannot; few items have the slots to themselves.
 inline int attn_chunk(const AttnWork* w, int n, int64_t kv_heads, int64_t slots, double each, double split,
-                      double join, int least, int grain) {
+                      double join, int least, double shared) {
   constexpr int kClasses = 12;   // sequences of similar length count as one class
   struct Class {
     double last, first, weight;
@@ -132,11 +132,12 @@ inline int attn_chunk(const AttnWork* w, int n, int64_t kv_heads, int64_t slots,
       const int parts = k.first < 0.75 * k.last ? 4 : 1;   // a causal prompt's tiles differ
       for (int q = 0; q < parts; ++q) {
         const double units = parts == 1 ? k.last : k.first + (k.last - k.first) * (q + 0.5) / parts;
-        const double run = double(int64_t((units / ns + grain - 0.01) / grain)) * grain;
-        deal.add((grain > 1 ? run : units / ns) * k.weight + over, (k.items * (q + 1) / parts - k.items * q / parts) * ns);
+        deal.add(units / ns * k.weight + over, (k.items * (q + 1) / parts - k.items * q / parts) * ns);
       }
     }
-    const double cost = deal.finish(slots) + (any ? join : 0);
+    double cost = deal.finish(slots);
+    if (shared > 0) cost = std::min(cost, shared * deal.finish(2 * slots));
+    if (any) cost += join;
     if (c == top || cost < best_cost) {
       best = c;
       best_cost = cost;
@@ -221,11 +222,13 @@ inline void attn_plan(AttnPlan& o, const KvView& c, const KvSeqs& s, int n_heads
   const double unit_bytes = double(c.dim) * elem_bytes * 2 * (1 << kDecodeUnitShift);
   const int dblocks = decode_blocks(c.dim, elem_bytes, o.decode_tile);
   const int dchunk = attn_chunk(dec, nd, c.kv_heads, dblocks * kAttnCUs, (dblocks == 2 ? 32768 : 98304) / unit_bytes,
-                                o.decode_rows * c.dim * 8 / unit_bytes, 98304 / unit_bytes, 2, 1);
+                                o.decode_rows * c.dim * 8 / unit_bytes, 98304 / unit_bytes, 2, 0);
   attn_fill(o.decode, dec, nd, dchunk, s, c.kv_heads, o.decode_tile, group);
-  // in units: 64 positions against 256 rows; a split item's sums are 256 fp32 rows written and read
-  const int64_t slots = c.dim == 64 ? 2 * kAttnCUs : kAttnCUs;
-  const int pchunk = prompt_items >= 16 * slots ? 1 << 30 : attn_chunk(pro, np, c.kv_heads, slots, 1.5, 2, 3, 4, 1);
+  // In units of 64 positions against 256 rows; a split item's sums are 256 fp32 rows written and read, and the
+  // join's launch counts for more of the shorter units of narrow heads.
+  const int pchunk = prompt_items >= 16 * kAttnCUs ? 1 << 30
+                                                   : attn_chunk(pro, np, c.kv_heads, kAttnCUs, 1.5, 2.5, 768.0 / c.dim, 4,
+                                                                c.dim == 64 ? 1.6 : 0);
   attn_fill(o.prompt, pro, np, pchunk, s, c.kv_heads, kPromptRows, group);
 
   size_t rows_o = 0, rows_ml = 0, score = 0, arrived = 0;
