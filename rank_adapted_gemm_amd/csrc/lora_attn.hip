@@ -17,7 +17,6 @@ namespace {
 
 constexpr int kBN = 1 << kPromptUnitShift;
 constexpr int kWaves = 8;   // 32 packed rows each; four bring keys, four values
-constexpr int kAhead = 4;   // fragments read ahead of the products
 
 // Values of a fragment: lane's column d = db * 32 + (lane & 31), eight positions of
 // 16-position step st in the order of the weights' registers.
@@ -70,6 +69,10 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
   using x8 = typename Vec<T>::x8;
   constexpr int BM = kWaves * 32, TILE = kBN * R::kBytes, KS = DIM / 16, DB = DIM / 32;
   constexpr int KR = F8 ? KS / 2 : KS;   // LDS reads of 32 positions' keys
+  // Fragments read ahead of the products.  256-wide heads: three, four take registers that the addresses
+  // need (a 4,096 window over 16,002 rows: 842 against 862 us); narrower ones: four (128-wide e4m3 prompt of
+  // 8,000 rows: 505 against 512 us).
+  constexpr int kAhead = DIM == 256 ? 3 : 4;
   static_assert(BM == kPromptRows, "one tile height for the host's plan");
   __shared__ __attribute__((aligned(1024))) char lds[4 * TILE];   // keys, keys, values, values
   __shared__ __attribute__((aligned(16))) int32_t bad[2][4];      // invalid 16-slot groups of a step

@@ -471,6 +471,24 @@ __global__ __launch_bounds__(256) void join_few_kernel(AttnArgs a, AttnPart part
   }
 }
 
+// Maximum and sum of one row over its splits, by one wave: lanes take splits, then meet.
+__device__ __forceinline__ void row_total(const float* part_ml, int64_t slot0, int64_t step, int nsplit, float& top,
+                                          float& total) {
+  const int lane = threadIdx.x & 63;
+  top = kLowest;
+  total = 0;
+  for (int i = lane; i < nsplit; i += 64) {
+    const f32x2 x = *reinterpret_cast<const f32x2*>(part_ml + (slot0 + i * step) * 2);
+    const float next = __builtin_fmaxf(top, x[0]);
+    total = total * __builtin_amdgcn_exp2f(top - next) + x[1] * __builtin_amdgcn_exp2f(x[0] - next);
+    top = next;
+  }
+  const float mine = top;
+  for (int d = 1; d < 64; d <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
+  total *= __builtin_amdgcn_exp2f(mine - top);
+  for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+}
+
 // One row by a block: each of its four waves reads a quarter of the splits.
 template <typename T, int DIM>
 __device__ __forceinline__ void join_one(const AttnArgs& a, const AttnSeq& sq, int64_t slot0, int64_t step, int head, int m,
@@ -479,15 +497,8 @@ __device__ __forceinline__ void join_one(const AttnArgs& a, const AttnSeq& sq, i
   typedef float vec __attribute__((ext_vector_type(PER)));
   __shared__ float acc[4][DIM];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  float top = kLowest;
-  for (int i = lane; i < sq.nsplit; i += 64) top = __builtin_fmaxf(top, a.part_ml[(slot0 + i * step) * 2]);
-  for (int d = 1; d < 64; d <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
-  float total = 0;
-  for (int i = lane; i < sq.nsplit; i += 64) {
-    const f32x2 x = *reinterpret_cast<const f32x2*>(a.part_ml + (slot0 + i * step) * 2);
-    total += x[1] * __builtin_amdgcn_exp2f(x[0] - top);
-  }
-  for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+  float top, total;
+  row_total(a.part_ml, slot0, step, sq.nsplit, top, total);
   vec sum = {};
 #pragma unroll 4
   for (int i = wave; i < sq.nsplit; i += 4) {
@@ -553,14 +564,8 @@ __global__ __launch_bounds__(256) void decode_finish_kernel(AttnArgs a, AttnPart
   if (__syncthreads_or(met)) {   // some position of the run is seen
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int m = wave; m < M; m += 4) {
-      float top = kLowest, total = 0;
-      for (int i = lane; i < sq.nsplit; i += 64) top = __builtin_fmaxf(top, a.part_ml[(slot0 + m + i * step) * 2]);
-      for (int d = 1; d < 64; d <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
-      for (int i = lane; i < sq.nsplit; i += 64) {
-        const f32x2 x = *reinterpret_cast<const f32x2*>(a.part_ml + (slot0 + m + i * step) * 2);
-        total += x[1] * __builtin_amdgcn_exp2f(x[0] - top);
-      }
-      for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+      float top, total;
+      row_total(a.part_ml, slot0 + m, step, sq.nsplit, top, total);
       if (lane == 0) lse[m] = total == 0 ? INFINITY : top + __builtin_log2f(total);   // nothing seen: no weight
     }
     __syncthreads();
