@@ -157,15 +157,21 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_mass_ke
       const bool masked = anybad || !(p0 + 31 <= ta && p0 + 31 < b1 &&
                                       (a.window < 0 || p0 >= tb - a.window + 1 || p0 + 31 < a.sinks));
       if (masked) {
-        const int t = time_of(na + col);
+        // a row past the last sees nothing; a position past the cache lies behind every row
+        const int t = ma + col < m1 ? time_of(na + col) : -1;
         const int low = a.window < 0 ? 0 : t - a.window + 1;
+        const int pl = p0 + hh * 4;
+        if (anybad) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            st[e] = __shfl(int(bad), (e >> 2) * 8 + hh * 4 + (e & 3)) ? __builtin_nanf("") : st[e];
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int pe = p0 + (e >> 2) * 8 + hh * 4 + (e & 3);
-          const bool isbad = __shfl(int(bad), pe - p0) != 0;
-          const bool seen = ma + col < m1 && pe < b1 && pe <= t && (pe >= low || pe < a.sinks);
-          const float x = isbad ? __builtin_nanf("") : __builtin_fmaf(st[e], c, -l);
-          acc[e] += seen ? __builtin_amdgcn_exp2f(x) : 0.0f;
+          const int pe = pl + (e >> 2) * 8 + (e & 3);
+          const bool seen = pe <= t && (pe >= low || pe < a.sinks);
+          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e], c, -l));
+          acc[e] += seen ? w : 0.0f;
         }
       } else {
 #pragma unroll
