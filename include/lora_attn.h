@@ -51,6 +51,11 @@
  * multiple of 16 up to 65536; n_seq <= LORA_MAX_SEGMENTS; kv_len <= 2^24;
  * n_heads <= 512; rows <= 2^24 and rows * n_heads < 2^31.
  *
+ * How a call runs.  Sequences of at most 32 packed rows (rows times heads that share a key-value
+ * head) are decoded; the rest are prompts, and a few short sequences beside them ride in their
+ * launch.  Long caches are split over blocks, whose sums meet in the workspace.  Results depend on
+ * the arguments alone: no order of arrival enters them.
+ *
  * Streams, ownership and errors are lora_proj.h's: calls are asynchronous on
  * `stream`, check every host argument before the first launch, allocate
  * nothing, keep nothing between calls, and return LORA_EHIP when a launch
@@ -127,8 +132,9 @@ lora_status lora_kv_append(const lora_kv_cache* cache, const lora_kv_batch* batc
  *               in an order that depends on the shapes alone; entries past kv_len[i] are left as
  *               they are.  mass_in may be mass_out itself, otherwise they must not overlap.
  *   mass_cap    at least the largest kv_len, when mass_out is given
- *   workspace   at least lora_attn_workspace_bytes(...) bytes of device scratch (NULL when 0);
- *               needs no initialisation; calls that share one must not overlap in time
+ *   workspace   at least lora_attn_workspace_bytes(...) bytes of device scratch (NULL when 0), for
+ *               this cache, batch, window and sinks; needs no initialisation; calls that share one
+ *               must not overlap in time, replays of a captured call included
  */
 lora_status lora_attn(const lora_kv_cache* cache, const lora_kv_batch* batch,
                       const void* q, int64_t q_row_stride, int64_t q_head_stride, int32_t n_heads,

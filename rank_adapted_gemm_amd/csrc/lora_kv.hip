@@ -8,7 +8,9 @@ namespace {
 //
 // A copy with an indirection, bound by bytes: every new row is read once and
 // written once.  A block takes kAppendRows consecutive rows, looks their pages
-// up once, and streams their k and v in 16-byte pieces.
+// up once, and streams their k and v in 16-byte pieces, kAppendDepth a thread at
+// a time (one at a time: 29 us).  16,002 rows of 4 heads of 256: 131 MB in 26.5 us,
+// 4.9 TB/s, as a large copy; 64 rows: 6.4 us, a launch and a load behind a load.
 constexpr int kAppendRows = 4;
 constexpr int kAppendDepth = 4;   // pieces a thread has under way
 
@@ -93,7 +95,9 @@ constexpr int kSelWaves = kSelThreads / 64;
 // first of those equal to it; first and last positions that stay anyway take the
 // highest key, which no weight has.  The last key is found by radix selection: a
 // histogram of its top bits in LDS, the bin that holds the budget's end, then the
-// next bits among the keys of that bin.  One block takes one (sequence, head).
+// next bits among the keys of that bin.  One block takes one (sequence, head):
+// 20 us for 24 of up to 32,013 weights (67 us with five passes over memory), 24 us
+// for 512 of up to 9,832.
 constexpr uint32_t kStays = 0xFFFFFFFFu;
 
 // Finds the bin, counting from the highest of n (2 a thread), where `k` keys are reached;
@@ -372,7 +376,8 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_long_kernel(EvictArg
 
 constexpr int kGatherRows = 64;
 
-// Copies kept rows to their new slots, and their weights; blockIdx.y is (sequence, head).
+// Copies kept rows to their new slots, and their weights; blockIdx.y is (sequence, head).  Bound by bytes:
+// 101 MB of 512-byte rows in 17 us (5.8 TB/s), 786 MB of 128-byte rows in 160 us (4.9 TB/s).
 __global__ __launch_bounds__(256) void evict_gather_kernel(EvictArgs a, int elem_bytes, uint32_t nan_word) {
   __shared__ int64_t src[kGatherRows], dst[kGatherRows];   // byte offsets; -1: no row, -2: source page invalid
   const int i = blockIdx.y / a.c.kv_heads, h = blockIdx.y - i * a.c.kv_heads;
