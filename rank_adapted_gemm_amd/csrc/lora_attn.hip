@@ -87,6 +87,7 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
   static_assert(BM == kPromptRows, "one tile height for the host's plan");
   __shared__ __attribute__((aligned(1024))) char lds[4 * TILE];   // keys, keys, values, values
   __shared__ __attribute__((aligned(16))) int32_t bad[2][4];      // invalid 16-slot groups of a step
+  __shared__ int32_t hit[2];                                      // steps (from 1) whose values held an infinity or NaN
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int hh = lane >> 5, col = lane & 31;
@@ -107,6 +108,7 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
   const int mw = m0 + wave * 32;
   const int tw_lo = t0 + mw / a.group, tw_hi = mw < m1 ? t0 + (min(m1, mw + 32) - 1) / a.group : -1;
   const int loww = a.window < 0 ? 0 : tw_lo - a.window + 1;        // first position in the window of the wave's first row
+  const int lowwx = a.window < 0 ? 0 : tw_hi - a.window + 1;       // of its last
   const int lowx = a.window < 0 ? 0 : t_hi - a.window + 1;         // and of the tile's last
   x8 q[KS];
   const float sc = a.scale * kLog2e * (F8 ? a.c.k_scale[item.head] : 1.0f);
@@ -270,6 +272,7 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
     return unit0 + kBN - 1 <= t_lo && (a.window < 0 || unit0 >= lowx || unit0 + kBN - 1 < a.sinks);
   };
 
+  if (tid < 2) hit[tid] = 0;
   load_pages(0);
   aim(0);
 #pragma unroll
@@ -323,7 +326,9 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
       const int p = unit0 + at / R::kBytes;
       seen |= p <= t_hi && (p >= pages.lo_pos || p < a.sinks);
     }
-    const bool dropped = __builtin_amdgcn_readfirstlane(__syncthreads_or(seen)) != 0;
+    if (__any(seen)) hit[buf] = it + 1;   // this step's mark
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
+    const bool dropped = __builtin_amdgcn_readfirstlane(hit[buf]) == it + 1;
 #pragma unroll 1
     for (int half = 0; half < kBN / 32; ++half) {
       const int p0 = unit0 + half * 32;
@@ -334,12 +339,15 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
       x8 w[2];
       scores(kt, st, [](int, int) {});
       const uint32_t badp = (anybad >> (2 * half)) & 3u;
+      // of a border step, a wave's rows often see all or nothing
+      if (badp != 0 || !(p0 + 31 <= tw_lo && (a.window < 0 || p0 >= lowwx || p0 + 31 < a.sinks))) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int p = p0 + (e >> 2) * 8 + hh * 4 + (e & 3);
-        const bool sees = p <= t && (p >= low || p < a.sinks);
-        const float x = (badp >> (e >> 3)) & 1u ? __builtin_nanf("") : st[e];
-        st[e] = sees ? x : -INFINITY;
+        for (int e = 0; e < 16; ++e) {
+          const int p = p0 + (e >> 2) * 8 + hh * 4 + (e & 3);
+          const bool sees = p <= t && (p >= low || p < a.sinks);
+          const float x = (badp >> (e >> 3)) & 1u ? __builtin_nanf("") : st[e];
+          st[e] = sees ? x : -INFINITY;
+        }
       }
       weights(st, w);
       outputs(kt + 2 * TILE, w, [](int, int) {});
