@@ -20,7 +20,7 @@
 // 256 over 4: 1.65 ms, 1.27 PFLOP/s (a large library product on the same card:
 // 1.35), matrix units busy for 66% of the cycles at 1.69 GHz, no LDS conflicts.
 // 8,000 rows of 32 heads of 128: 477 us, 1.10 PFLOP/s.  At 64-wide heads the
-// exponentials are the larger part: 8,000 rows of 16 heads, 190 us, 0.69 PFLOP/s.
+// exponentials are the larger part: 8,000 rows of 16 heads, 186 us, 0.70 PFLOP/s.
 #include "lora_attn_core.h"
 
 namespace lora {
@@ -286,6 +286,10 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
       meet();
       if (((it + 1) & 63) == 0) load_pages(it + 1);
       aim(it + 1);
+      // Waves w and w + 4 share a SIMD and leave the barrier together.  At 64-wide heads, where a step is
+      // short and mostly exponentials, 128 cycles' delay of one lets its products run beside the other's
+      // exponentials (8,000 rows of 16 heads: 191 -> 186 us; wider heads gain nothing).
+      if (DIM == 64 && wave >= 4) __builtin_amdgcn_s_sleep(2);
       f32x16 st;
       x8 w[2];
       scores(kt, st, [&](int n, int of) {
