@@ -7,12 +7,16 @@
 // registers, as the first operand of the product, and two of them share a half of
 // the rows of a step, which DMA loads bring to LDS one step ahead.  Early
 // positions are seen by every row, so a block's length is what a launch can last:
-// 64 positions keep it at half of what 128 would.  Sums stay in one block, so
-// their order depends on the shapes alone.
+// 64 positions keep it at half of what 128 would, and where few heads or sinks
+// leave CUs idle beside long ones, several blocks share the rows of a block of
+// positions and a second launch adds their sums in order.  Which order depends on
+// the shapes alone.
 //
 // Measured: six prompts of up to 2,022 rows, 16 heads of 64, 28 us (50 us with 128
-// positions a block and rows through registers); 4,000 rows and a suffix of 500
-// behind 8,500 positions, 32 heads of 128, about 230 us for 0.10 PFLOP.
+// positions a block and rows through registers).  With the attention before it:
+// 4,000 rows and a suffix of 500 behind 8,500 positions, 16 heads of 256 over 4,
+// 428 us (567 us with one block for all rows of 64 positions); three prompts of up
+// to 2,176 rows, 5 heads of 128 over 1 under a window with sinks, 51 us (192 us).
 #include "lora_attn_core.h"
 
 namespace lora {
@@ -30,7 +34,7 @@ template <typename T, bool F8, int DIM>
 __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_mass_kernel(AttnArgs a, AttnPart part) {
   using Q = Row<false, DIM>;   // rows of q are 16 bits wide whatever the cache holds
   using x8 = typename Vec<T>::x8;
-  constexpr int KS = DIM / 16, QN = DIM == 256 ? 64 : 128, QW = QN / 2;   // rows of a step, of a wave in it
+  constexpr int KS = DIM / 16, QN = mass_step_rows(DIM), QW = QN / 2;   // rows of a step, of a wave in it
   constexpr int TILE = QN * Q::kBytes, LOADS = TILE / 1024 / kWaves;
   constexpr int AHEAD = 4;
   __shared__ __attribute__((aligned(1024))) char lds[2 * TILE];
@@ -38,15 +42,18 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_mass_ke
   const int hh = lane >> 5, col = lane & 31, qg = wave >> 1;
   const int s = seq_of_item(part, blockIdx.x);
   const AttnSeq sq = part.seq[s];
-  const int r = int(blockIdx.x) - (s == 0 ? 0 : part.seq[s - 1].item_end);
-  const int head = r % a.c.kv_heads, b0 = r / a.c.kv_heads * kMassRows;   // early positions, which most rows see, first
+  const int r = int(blockIdx.x) - (s == 0 ? 0 : part.seq[s - 1].item_end), per = r / a.c.kv_heads;
+  const int head = r - per * a.c.kv_heads, split = per % sq.nsplit;
+  const int b0 = per / sq.nsplit * kMassRows;   // early positions, which most rows see, first
   const int t0 = sq.kv_len - sq.rows;
   const int b1 = min(sq.kv_len, b0 + kMassRows);
-  // rows that see some of positions b0 .. b1 - 1
-  const int j0 = max(0, b0 - t0);
-  const int j1 = a.window < 0 || b0 < a.sinks ? sq.rows
-                                              : int(min(int64_t(sq.rows), max(int64_t(0), int64_t(b1) - 1 + a.window - t0)));
-  const int m0 = j0 * a.group, m1 = j1 * a.group;
+  const RowRange seen = rows_that_see(b0, b1, sq.rows, sq.kv_len, a.window, a.sinks);
+  const int splits = mass_splits(seen, a.group, QN, part.mass_steps, sq.nsplit);
+  if (split >= splits) return;
+  // the item's packed rows: whole steps of those that see the block
+  const int mfirst = seen.first * a.group, mend = seen.end * a.group, steps = (mend - mfirst + QN - 1) / QN;
+  const int m0 = mfirst + split_begin(steps, split, splits) * QN;
+  const int m1 = min(mend, mfirst + split_begin(steps, split + 1, splits) * QN);
   const int p0 = b0 + (wave & 1) * 32, p = p0 + col;
   const Pages pages = pages_of(a, sq.index, t0, sq.kv_len - 1);
 
@@ -85,7 +92,7 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_mass_ke
   const uint32_t lds0 = lds_addr(lds);
   const int lrow = lane / Q::kChunks, lslot = lane % Q::kChunks;
   constexpr int RPL = Q::kRowsPerLoad;
-  uint32_t j = uint32_t(j0), h = 0;
+  uint32_t j = uint32_t(m0) / group, h = uint32_t(m0) - j * group;
   auto advance = [&] {
     h += QN;
     const uint32_t dj = over(h);
@@ -198,9 +205,33 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_mass_ke
   if (qg == 1 && col < 16) other[(wave & 1) * 32 + place] = mine;
   __syncthreads();
   if (qg == 0 && col < 16 && p0 + place < b1) {
+    const float both = mine + other[(wave & 1) * 32 + place];
+    if (splits > 1) {
+      a.part_o[int64_t(blockIdx.x) * kMassRows + (p0 - b0) + place] = both;
+      return;
+    }
     const int64_t at = (int64_t(sq.index) * a.c.kv_heads + head) * a.mass_cap + p0 + place;
-    a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.0f) + (mine + other[(wave & 1) * 32 + place]);
+    a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.0f) + both;
   }
+}
+
+// Positions whose rows several items shared: their sums, in the items' order.
+__global__ __launch_bounds__(256) void mass_join_kernel(AttnArgs a, AttnPart part, int step_rows) {
+  const int s = blockIdx.z, head = blockIdx.y;
+  const AttnSeq sq = part.seq[s];
+  const int first = s == 0 ? 0 : part.seq[s - 1].item_end;
+  const int p = int(blockIdx.x) * 256 + int(threadIdx.x);
+  if (p >= sq.kv_len) return;
+  const int block = p / kMassRows, b0 = block * kMassRows, b1 = min(sq.kv_len, b0 + kMassRows);
+  const int splits = mass_splits(rows_that_see(b0, b1, sq.rows, sq.kv_len, a.window, a.sinks), a.group, step_rows,
+                                 part.mass_steps, sq.nsplit);
+  if (splits == 1) return;
+  const float* src = a.part_o + (int64_t(first) + int64_t(block) * sq.nsplit * a.c.kv_heads + head) * kMassRows + (p - b0);
+  float sum = 0;
+#pragma unroll 4
+  for (int i = 0; i < splits; ++i) sum += src[int64_t(i) * a.c.kv_heads * kMassRows];
+  const int64_t at = (int64_t(sq.index) * a.c.kv_heads + head) * a.mass_cap + p;
+  a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.0f) + sum;
 }
 
 template <typename T, bool F8>
@@ -223,6 +254,15 @@ hipError_t launch_attn_mass_prompt(const AttnArgs& a, const AttnPart& p, int dty
     if (f8) run_mass<_Float16, true>(a, p, stream);
     else run_mass<_Float16, false>(a, p, stream);
   }
+  hipError_t e = hipGetLastError();
+  int longest = 0, splits = 1;
+  for (int i = 0; i < p.n; ++i) {
+    longest = p.seq[i].kv_len > longest ? p.seq[i].kv_len : longest;
+    splits = p.seq[i].nsplit > splits ? p.seq[i].nsplit : splits;
+  }
+  if (e != hipSuccess || splits == 1) return e;
+  hipLaunchKernelGGL(mass_join_kernel, dim3((longest + 255) / 256, a.c.kv_heads, p.n), dim3(256), 0, stream, a, p,
+                     mass_step_rows(a.c.dim));
   return hipGetLastError();
 }
 

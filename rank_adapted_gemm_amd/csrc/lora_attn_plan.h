@@ -161,7 +161,7 @@ inline void attn_fill(AttnPath& path, AttnWork* w, int n, int chunk, const KvSeq
     AttnPart& p = path.part[path.parts];
     int& join = path.join_rows[path.parts];
     p.n = std::min(kAttnSeqs, n - at);
-    p.items = p.split_items = p.score_cols = join = 0;
+    p.items = p.split_items = p.score_cols = p.mass_steps = join = 0;
     for (int i = 0; i < p.n; ++i) {
       const AttnWork& x = w[at + i];
       p.items += x.rows == 0 ? 0 : x.tiles * x.nsplit * kv_heads;
@@ -173,6 +173,50 @@ inline void attn_fill(AttnPath& path, AttnWork* w, int n, int chunk, const KvSeq
       if (x.rows > 0)
         p.score_cols = std::max(p.score_cols, (x.units_last + x.nsplit - 1) / x.nsplit << kDecodeUnitShift);
     }
+  }
+}
+
+// The prompts' weights: an item per 64 positions and head, and several where the longest would last much
+// longer than an even share of all.
+inline void attn_mass_part(AttnPart& p, const KvView& c, int group, int window, int sinks) {
+  const int step = mass_step_rows(c.dim);
+  double total = 0;
+  int64_t longest = 1;
+  for (int i = 0; i < p.n; ++i) {
+    const AttnSeq& s = p.seq[i];
+    const int blocks = (s.kv_len + kMassRows - 1) / kMassRows;
+    auto steps = [&](int b) {
+      const int b0 = b * kMassRows, b1 = std::min(s.kv_len, b0 + kMassRows);
+      const RowRange r = rows_that_see(b0, b1, s.rows, s.kv_len, window, sinks);
+      return (int64_t(r.end - r.first) * group + step - 1) / step;
+    };
+    // Every row may see the first block; else the blocks about the first new row are seen most: rows come
+    // into a window one by one before it, and leave after it.  These, one in the middle of the new rows and
+    // the last stand for all.
+    const int mid = (s.kv_len - s.rows) / kMassRows, at[5] = {0, mid, std::min(blocks - 1, mid + 1),
+                                                              std::min(blocks - 1, (s.kv_len - s.rows / 2) / kMassRows),
+                                                              blocks - 1};
+    int64_t most = 0, sum = 0;
+    for (int k = 0; k < 5; ++k) {
+      const int64_t n = steps(std::min(blocks - 1, at[k]));
+      most = std::max(most, n);
+      if (k > 0) sum += n;
+    }
+    longest = std::max(longest, most);
+    total += 0.25 * double(sum) * blocks * c.kv_heads;
+    p.seq[i].nsplit = int(std::min<int64_t>(most, 1 << 20));   // the steps, for now
+  }
+  const double share = total / (2 * kAttnCUs);   // two blocks keep a CU busy
+  const int64_t most = std::max<int64_t>(4, int64_t(share) + 1);
+  p.mass_steps = longest <= most + most / 2 ? 0x7FFFFFFF : int(std::min<int64_t>(most, 1 << 20));
+  p.items = 0;
+  for (int i = 0; i < p.n; ++i) {
+    AttnSeq& s = p.seq[i];
+    const int64_t blocks = int64_t((s.kv_len + kMassRows - 1) / kMassRows) * c.kv_heads;
+    const int64_t splits = s.nsplit <= p.mass_steps ? 1 : (s.nsplit + p.mass_steps - 1) / p.mass_steps;
+    s.nsplit = int(std::max<int64_t>(1, std::min(splits, 65536 / std::max<int64_t>(1, blocks))));
+    p.items += int(blocks * s.nsplit);
+    s.item_end = p.items;
   }
 }
 
@@ -231,7 +275,7 @@ inline void attn_plan(AttnPlan& o, const KvView& c, const KvSeqs& s, int n_heads
                                                                 c.dim == 64 ? 1.6 : 0);
   attn_fill(o.prompt, pro, np, pchunk, s, c.kv_heads, kPromptRows, group);
 
-  size_t rows_o = 0, rows_ml = 0, score = 0, arrived = 0;
+  size_t rows_o = 0, rows_ml = 0, score = 0, arrived = 0, sums = 0;   // sums: of weights, after the joins
   for (int i = 0; i < o.decode.parts; ++i) {
     const AttnPart& p = o.decode.part[i];
     rows_o = std::max(rows_o, size_t(p.split_items) * o.decode_tile);
@@ -246,6 +290,11 @@ inline void attn_plan(AttnPlan& o, const KvView& c, const KvSeqs& s, int n_heads
     const AttnPart& p = o.prompt.part[i];
     rows_o = std::max(rows_o, size_t(p.split_items) * kPromptRows);
     rows_ml = std::max(rows_ml, size_t(p.split_items) * kPromptRows);
+    if (mass) {
+      AttnPart m = p;
+      attn_mass_part(m, c, group, window, sinks);
+      if (m.mass_steps != 0x7FFFFFFF) sums = std::max(sums, size_t(m.items) * kMassRows * 4);
+    }
   }
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   o.off_lse = 0;
@@ -253,16 +302,7 @@ inline void attn_plan(AttnPlan& o, const KvView& c, const KvSeqs& s, int n_heads
   o.off_scores = o.off_ml + up(rows_ml * 8);
   o.off_arrived = o.off_scores + up(score);
   o.off_o = o.off_arrived + up(arrived);
-  o.bytes = o.off_o + up(rows_o * c.dim * 4);
-}
-
-// The prompts' weight blocks: the same sequences, an item per 128 positions and head.
-inline void attn_mass_part(AttnPart& p, int kv_heads) {
-  p.items = 0;
-  for (int i = 0; i < p.n; ++i) {
-    p.items += (p.seq[i].kv_len + kMassRows - 1) / kMassRows * kv_heads;
-    p.seq[i].item_end = p.items;
-  }
+  o.bytes = o.off_o + up(std::max(rows_o * c.dim * 4, sums));
 }
 
 }  // namespace lora

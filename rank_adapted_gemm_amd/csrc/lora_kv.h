@@ -94,6 +94,7 @@ struct AttnPart {
   int32_t n;
   int32_t items, split_items;    // items of sequences with nsplit > 1 come first
   int32_t score_cols;            // decode: positions of an item's score rows in the workspace
+  int32_t mass_steps;            // prompts' weights: steps of rows an item takes at most
   AttnSeq seq[kAttnSeqs];
 };
 
@@ -153,6 +154,28 @@ struct AttnArgs {
   float scale;
 };
 
+// Rows of a step of the prompts' weight kernel.
+__host__ __device__ constexpr int mass_step_rows(int dim) { return dim == 256 ? 64 : 128; }
+
+// Rows [first, end) of a sequence that see some of positions b0 .. b1 - 1.
+struct RowRange {
+  int32_t first, end;
+};
+__host__ __device__ inline RowRange rows_that_see(int b0, int b1, int rows, int kv_len, int window, int sinks) {
+  const int t0 = kv_len - rows;
+  const int64_t last = int64_t(b1) - 1 + window - t0;   // a window's rows end there
+  const int end = window < 0 || b0 < sinks ? rows : int(last < 0 ? 0 : (last < rows ? last : rows));
+  const int first = b0 > t0 ? b0 - t0 : 0;
+  return RowRange{first, end > first ? end : first};
+}
+
+// Items that share a block of positions, at most `most`: the rows that see it in runs of mass_steps steps.
+__host__ __device__ inline int mass_splits(RowRange r, int group, int step_rows, int mass_steps, int most) {
+  const int64_t steps = (int64_t(r.end - r.first) * group + step_rows - 1) / step_rows;
+  const int64_t n = steps <= mass_steps ? 1 : (steps + mass_steps - 1) / mass_steps;
+  return n < most ? int(n) : most;
+}
+
 // Shapes of the two attention kernels.
 constexpr int kDecodeUnitShift = 5;   // 32 positions, one wave's step
 constexpr int kPromptUnitShift = 6;   // 64 positions, one block's step
@@ -182,6 +205,7 @@ hipError_t launch_attn_decode(const AttnArgs& a, const AttnPart& p, int rows, in
                               hipStream_t stream);
 hipError_t launch_attn_join(const AttnArgs& a, const AttnPart& p, int tile_rows, int most, int dtype,
                             hipStream_t stream);
+// p.items: the launch's items, in seq[].item_end; sums of positions that several items share go to part_o.
 hipError_t launch_attn_mass_prompt(const AttnArgs& a, const AttnPart& p, int dtype, int cache_dtype,
                                    hipStream_t stream);
 hipError_t launch_attn_decode_finish(const AttnArgs& a, const AttnPart& p, int tile_rows, int rows, int dtype,

@@ -260,7 +260,7 @@ lora_status lora_attn(const lora_kv_cache* cache, const lora_kv_batch* batch,
     if (e == hipSuccess && p.split_items > 0)
       e = lora::launch_attn_join(a, p, lora::kPromptRows, plan.prompt.join_rows[i], dtype, stream);
     if (e == hipSuccess && mass_out) {
-      lora::attn_mass_part(p, a.c.kv_heads);
+      lora::attn_mass_part(p, a.c, a.group, window, sinks);
       e = lora::launch_attn_mass_prompt(a, p, dtype, cache->dtype, stream);
     }
   }

@@ -135,3 +135,30 @@ def test_many_sequences():
     got = values(mass)
     for i, n in enumerate(lens):
         np.testing.assert_allclose(got[i, :, :n], ref["mass"][i, :, :n], rtol=1e-4, atol=1e-7)
+
+
+@pytest.mark.parametrize("rows,lens,heads,kv,dim,window,sinks", [
+    ([900], [900], 5, 1, 64, 90, 20),            # sinks that every row sees beside positions few rows see
+    ([700, 40], [1500, 300], 8, 1, 128, -1, 0),  # one head: several blocks share the rows of a block of positions
+    ([300], [300], 16, 2, 256, -1, 0),
+    ([500, 1, 33], [500, 700, 33], 6, 2, 64, 200, 70),
+])
+def test_weights_summed_over_blocks(rows, lens, heads, kv, dim, window, sinks):
+    p = Problem(71, rows, lens, heads, kv, dim, 16)
+    c, b = p.make()
+    cap = max(lens)
+    start = torch.rand(len(lens), kv, cap, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+    out = [torch.full_like(start, -1.0) for _ in range(2)]
+    ws = ra.attn_workspace(c, b, heads, window, sinks, mass=True)
+    for o in out:
+        ws.fill_(0xFF)
+        ra.attn(c, b, p.q, window=window, sinks=sinks, mass=start, mass_out=o, workspace=ws)
+    assert torch.equal(out[0], out[1])
+    ref = p.reference(window=window, sinks=sinks)
+    got, base, rel = values(out[0]), values(start), float(np.max(weight_error(ref, dim)))
+    for i, n in enumerate(lens):
+        want = base[i, :, :n] + ref["mass"][i, :, :n]
+        # each weight's error, and a rounding for each term of the sum and the total's own
+        tol = rel * ref["mass"][i, :, :n] + (max(rows) * heads // kv + 2) * 2.0 ** -24 * want
+        assert (np.abs(got[i, :, :n] - want) <= tol).all()
+        assert (got[i, :, n:] == -1.0).all()
