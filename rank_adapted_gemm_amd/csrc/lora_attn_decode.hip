@@ -476,22 +476,23 @@ __global__ __launch_bounds__(256) void join_few_kernel(AttnArgs a, AttnPart part
   }
 }
 
-// Maximum and sum of one row over its splits, by one wave: lanes take splits, then meet.
+// Maximum and sum of one row over its splits, by LANES neighbouring lanes: they take splits, then meet.
+template <int LANES>
 __device__ __forceinline__ void row_total(const float* part_ml, int64_t slot0, int64_t step, int nsplit, float& top,
                                           float& total) {
-  const int lane = threadIdx.x & 63;
   top = kLowest;
   total = 0;
-  for (int i = lane; i < nsplit; i += 64) {
+#pragma unroll 4
+  for (int i = threadIdx.x & (LANES - 1); i < nsplit; i += LANES) {
     const f32x2 x = *reinterpret_cast<const f32x2*>(part_ml + (slot0 + i * step) * 2);
     const float next = __builtin_fmaxf(top, x[0]);
     total = total * __builtin_amdgcn_exp2f(top - next) + x[1] * __builtin_amdgcn_exp2f(x[0] - next);
     top = next;
   }
   const float mine = top;
-  for (int d = 1; d < 64; d <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
+  for (int d = 1; d < LANES; d <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
   total *= __builtin_amdgcn_exp2f(mine - top);
-  for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+  for (int d = 1; d < LANES; d <<= 1) total += __shfl_xor(total, d);
 }
 
 // One row by a block: each of its four waves reads a quarter of the splits.
@@ -503,7 +504,7 @@ __device__ __forceinline__ void join_one(const AttnArgs& a, const AttnSeq& sq, i
   __shared__ float acc[4][DIM];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   float top, total;
-  row_total(a.part_ml, slot0, step, sq.nsplit, top, total);
+  row_total<64>(a.part_ml, slot0, step, sq.nsplit, top, total);
   vec sum = {};
 #pragma unroll 4
   for (int i = wave; i < sq.nsplit; i += 4) {
@@ -567,11 +568,10 @@ __global__ __launch_bounds__(256) void decode_finish_kernel(AttnArgs a, AttnPart
   const bool met = p < sq.kv_len && (unit < units.sinks || (u >= units.sinks && u < units.count));
   float sum = 0;
   if (__syncthreads_or(met)) {   // some position of the run is seen
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int m = wave; m < M; m += 4) {
+    for (int m = threadIdx.x >> 4; m < M; m += 16) {   // sixteen rows at a time
       float top, total;
-      row_total(a.part_ml, slot0 + m, step, sq.nsplit, top, total);
-      if (lane == 0) lse[m] = total == 0 ? INFINITY : top + __builtin_log2f(total);   // nothing seen: no weight
+      row_total<16>(a.part_ml, slot0 + m, step, sq.nsplit, top, total);
+      if ((threadIdx.x & 15) == 0) lse[m] = total == 0 ? INFINITY : top + __builtin_log2f(total);   // nothing seen: no weight
     }
     __syncthreads();
     if (met) {
