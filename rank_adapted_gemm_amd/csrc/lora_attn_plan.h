@@ -29,7 +29,6 @@ struct AttnPlan {
 // A sequence's work for one kernel.
 struct AttnWork {
   int index, rows, units_last, units_first, tiles, nsplit;
-  double weight;   // a unit's cost: a tile with few waves at work takes its steps faster
 };
 
 // When a launch's items, dealt out from the longest to the slot that is free first, are all done.  Items
@@ -99,7 +98,7 @@ inline int attn_chunk(const AttnWork* w, int n, int64_t kv_heads, int64_t slots,
                       double join, int least, double shared) {
   constexpr int kClasses = 12;   // sequences of similar length count as one class
   struct Class {
-    double last, first, weight;
+    double last, first;
     int64_t items;
   };
   Class cls[kClasses];
@@ -108,15 +107,14 @@ inline int attn_chunk(const AttnWork* w, int n, int64_t kv_heads, int64_t slots,
   const int per = (n + kClasses - 1) / kClasses;
   for (int i = 0; i < n; i += per, ++classes) {   // w: longest first
     Class& k = cls[classes];
-    k = Class{0, 0, 0, 0};
+    k = Class{0, 0, 0};
     const int m = std::min(per, n - i);
     for (int j = i; j < i + m; ++j) {
       k.last += double(w[j].units_last) / m;
       k.first += double(w[j].units_first) / m;
-      k.weight += w[j].weight / m;
       k.items += int64_t(w[j].tiles) * kv_heads;
       top = std::max(top, w[j].units_last);
-      total += 0.5 * (double(w[j].units_last) + w[j].units_first) * w[j].tiles * kv_heads * w[j].weight;
+      total += 0.5 * (double(w[j].units_last) + w[j].units_first) * w[j].tiles * kv_heads;
     }
   }
   int best = top;
@@ -132,7 +130,7 @@ inline int attn_chunk(const AttnWork* w, int n, int64_t kv_heads, int64_t slots,
       const int parts = k.first < 0.75 * k.last ? 4 : 1;   // a causal prompt's tiles differ
       for (int q = 0; q < parts; ++q) {
         const double units = parts == 1 ? k.last : k.first + (k.last - k.first) * (q + 0.5) / parts;
-        deal.add(units / ns * k.weight + over, (k.items * (q + 1) / parts - k.items * q / parts) * ns);
+        deal.add(units / ns + over, (k.items * (q + 1) / parts - k.items * q / parts) * ns);
       }
     }
     double cost = deal.finish(slots);
@@ -227,8 +225,8 @@ inline void attn_plan(AttnPlan& o, const KvView& c, const KvSeqs& s, int n_heads
   const int group = n_heads / c.kv_heads;
   o.decode_rows = 0;
   int64_t prompt_items = 0;
-  // Beside prompts, a few short sequences ride in their launch: a tile with one wave at work costs a step
-  // about as long as its bytes take, less than launches of their own.
+  // Beside prompts, a few short sequences ride in their launch: a step of a few rows takes as long as one of
+  // 256, but less of the chip than launches of their own.
   int64_t short_units = 0;
   bool prompts = false;
   for (int i = 0; i < s.n; ++i) {
@@ -243,15 +241,14 @@ inline void attn_plan(AttnPlan& o, const KvView& c, const KvSeqs& s, int n_heads
     const int64_t packed = int64_t(rows) * group;
     if (packed <= kAttnDecodeMaxRows && !(ride && rows > 0)) {
       const Units u = units_of(len - rows, len - 1, window, sinks, kDecodeUnitShift);
-      dec[nd++] = AttnWork{i, rows, rows == 0 ? 1 : u.count, rows == 0 ? 0 : u.count, 1, 1, 1.0};
+      dec[nd++] = AttnWork{i, rows, rows == 0 ? 1 : u.count, rows == 0 ? 0 : u.count, 1, 1};
       o.decode_rows = std::max(o.decode_rows, int(packed));
     } else {
       const int tiles = int((packed + kPromptRows - 1) / kPromptRows);
       const int last_row = int(int64_t(tiles - 1) * kPromptRows / group), first_end = std::min(rows, (kPromptRows - 1) / group + 1);
       const Units a = units_of(len - rows + last_row, len - 1, window, sinks, kPromptUnitShift);
       const Units b = units_of(len - rows, len - rows + first_end - 1, window, sinks, kPromptUnitShift);
-      pro[np++] = AttnWork{i, rows, std::max(a.count, b.count), std::min(a.count, b.count), tiles, 1,
-                           packed <= kPromptRows / 2 ? 0.5 : 1.0};
+      pro[np++] = AttnWork{i, rows, std::max(a.count, b.count), std::min(a.count, b.count), tiles, 1};
       prompt_items += int64_t(tiles) * c.kv_heads;
     }
   }
