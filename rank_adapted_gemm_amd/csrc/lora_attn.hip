@@ -223,8 +223,8 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
 #pragma unroll
     for (int e = 1; e < 16; ++e) mx = __builtin_fmaxf(mx, st[e]);
     mx = max_halves(mx) * c;
-    if (__any(mx > top + kLag)) {
-      const float next = __builtin_fmaxf(top, mx), keep = __builtin_amdgcn_exp2f(top - next);
+    if (__any(ahead<T>(mx, top))) {
+      const float next = next_reference<T>(mx, top), keep = __builtin_amdgcn_exp2f(top - next);
       top = next;
       sum *= keep;
 #pragma unroll

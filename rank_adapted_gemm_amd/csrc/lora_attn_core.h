@@ -18,9 +18,29 @@ struct Vec {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.4028234663852886e38f;   // a running maximum before any score: finite, so differences are not NaN
-// A running maximum may lag behind by this many powers of two before sums and outputs are
-// rescaled: weights stay below 2^8, which every type holds, and the quotient is the same.
-constexpr float kLag = 8.0f;
+// Weights are taken against a reference below the running maximum: 2^(score - reference), the same quotient.
+// A weight meets the values in their type.  fp16's smallest step is 2^-24, so there the largest weight stands at
+// 2^11 or above, and one that is rounded to nothing is below 2^-36 of it: behind one heavy position, 2^24 light
+// ones lose less than half of the output's half step (with the largest at 1, 32,768 of them could lose 0.1%).
+// bf16 has fp32's exponents and needs no lead.
+template <typename T>
+constexpr float kLead = __is_same(T, __bf16) ? 0.0f : 11.0f;
+// The maximum may run ahead of the reference by this many more powers of two before sums and outputs are
+// rescaled: weights stay within 2^15 in fp16, whose largest value is just below 2^16, and 2^8 in bf16.
+template <typename T>
+constexpr float kLag = __is_same(T, __bf16) ? 8.0f : 4.0f;
+
+// The maximum mx has left the reference behind.  (As a difference, which is exact where the two are close.)
+template <typename T>
+__device__ __forceinline__ bool ahead(float mx, float ref) { return mx - ref > kLead<T> + kLag<T>; }
+
+// The reference for a maximum of mx, never below the last one.
+template <typename T>
+__device__ __forceinline__ float next_reference(float mx, float ref) {
+  float next = mx - kLead<T>;
+  if (kLead<T> > 0 && mx - next > kLead<T> + kLag<T>) next = mx;   // scores of 2^27 and above are 16 apart
+  return __builtin_fmaxf(ref, next);
+}
 
 template <typename T>
 __device__ __forceinline__ f32x16 mfma32(typename Vec<T>::x8 a, typename Vec<T>::x8 b, f32x16 c) {

@@ -299,8 +299,8 @@ __global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16
 #pragma unroll
       for (int e = 1; e < 4; ++e) mx = __builtin_fmaxf(mx, __builtin_fmaxf(st[x][0][e], st[x][1][e]));
       mx = max_rows16(max_halves(mx)) * c;
-      if (__any(mx > top[x] + kLag)) {
-        const float next = __builtin_fmaxf(top[x], mx), keep = __builtin_amdgcn_exp2f(top[x] - next);
+      if (__any(ahead<T>(mx, top[x]))) {
+        const float next = next_reference<T>(mx, top[x]), keep = __builtin_amdgcn_exp2f(top[x] - next);
         top[x] = next;
         sum[x] *= keep;
 #pragma unroll
