@@ -44,8 +44,10 @@
  * Precision.  q, out and new rows are bf16 or fp16.  The cache holds the same
  * type, or e4m3 (OCP, largest value 448) with one fp32 scale per key-value head
  * for k and for v: value = code * scale.  Scores, the softmax's statistics,
- * sums over positions and accumulated weights are fp32; the weights are rounded
- * to q's type before they meet v; out is rounded once at the store.
+ * sums over positions and accumulated weights are fp32; out is rounded once at
+ * the store.  Before they meet v, decoded rows' weights are split into two
+ * numbers of q's type, which hold twice its bits; prompts' weights are rounded
+ * to q's type once.
  *
  * Limits (LORA_EUNSUPPORTED beyond): head_dim 64, 128 or 256; page_size a
  * multiple of 16 up to 65536; n_seq <= LORA_MAX_SEGMENTS; kv_len <= 2^24;

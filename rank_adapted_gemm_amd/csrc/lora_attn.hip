@@ -240,7 +240,9 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
       const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e + 1], c, -top));
       add += w0;
       add += w1;
-      pk[e >> 3][(e >> 1) & 3] = pack_pair<T>(w0, w1);   // the weights' one rounding, to the type of the product
+      // The weights' one rounding, to the type of the product: matrix units bound this kernel, and a second
+      // product with the remainders, as decoded rows have, takes 2,265 instead of 1,612 us at 16,002 rows.
+      pk[e >> 3][(e >> 1) & 3] = pack_pair<T>(w0, w1);
     }
     sum += add;
     w[0] = __builtin_bit_cast(x8, pk[0]);

@@ -1,5 +1,6 @@
-"""How much of a weight survives the product with the values: weights far below the largest one, and scores
-whose steps are wide.  The fp64 reference of tests/attn_util.py; bounds counted here."""
+"""How much of a weight survives the product with the values: weights far below the largest one, scores whose
+steps are wide, and decoded rows' weights past their first rounding.  The fp64 reference of
+tests/attn_util.py; bounds counted here."""
 import numpy as np
 import pytest
 import torch
@@ -67,3 +68,19 @@ def test_scores_whose_steps_are_wider_than_the_weights_range(rows, dtype):
     # a mean of values in [1, 2], a half step for each weight and one for the store
     h = HALF_STEP[dtype]
     assert torch.isfinite(y).all() and y.min() >= 1 - 2.1 * h and y.max() <= 2 * (1 + 2.1 * h)
+
+
+@pytest.mark.parametrize("dtype,cache", [("bf16", None), ("f16", None), ("bf16", "e4m3"), ("f16", "e4m3")])
+@pytest.mark.parametrize("rows,lens,heads,kv,dim,window,sinks", [
+    ([1], [37], 4, 1, 64, -1, 0), ([1, 1, 1], [310, 65, 900], 16, 4, 256, -1, 0), ([1, 2, 4], [700, 2, 400], 8, 2, 128, -1, 0),
+    ([4], [1300], 8, 1, 64, 500, 9), ([1], [9000], 4, 1, 128, -1, 0), ([4, 1], [90, 1000], 16, 2, 256, -1, 0)])
+@pytest.mark.parametrize("mass", [False, True])
+def test_decoded_rows_lose_no_weight_to_the_product_type(mass, rows, lens, heads, kv, dim, window, sinks, dtype, cache):
+    """A decoded weight enters the product as its rounding to q's type and the rounded remainder: half a step of
+    half a step is lost."""
+    p = Problem(77 + dim, rows, lens, heads, kv, dim, 48, dtype, cache)
+    c, b = p.make()
+    out = torch.zeros(len(lens), kv, max(lens), device="cuda") if mass else None
+    y = ra.attn(c, b, p.q, window=window, sinks=sinks, mass_out=out)
+    check_against(y, p.reference(window=window, sinks=sinks), dtype, dim, HALF_STEP[dtype] ** 2,
+                  2.0 ** -36 if dtype == "f16" else 0.0)
