@@ -47,7 +47,7 @@
  * sums over positions and accumulated weights are fp32; out is rounded once at
  * the store.  Before they meet v, decoded rows' weights are split into two
  * numbers of q's type, which hold twice its bits; prompts' weights are rounded
- * to q's type once.
+ * once, to q's type, or to fp16 over an E4M3 cache.
  *
  * Limits (LORA_EUNSUPPORTED beyond): head_dim 64, 128 or 256; page_size a
  * multiple of 16 up to 65536; n_seq <= LORA_MAX_SEGMENTS; kv_len <= 2^24;

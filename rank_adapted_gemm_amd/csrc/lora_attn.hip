@@ -73,11 +73,24 @@ struct ValueReader {
   }
 };
 
+// The type in which weights meet values: the queries', or fp16 over e4m3 pages, which holds every code and three
+// more bits of a weight than bf16 (8,000 rows of 32 heads of 128: 509 against 497 us, an eighth of the error).
+template <typename T, bool F8>
+struct WeightType {
+  using type = T;
+};
+template <>
+struct WeightType<__bf16, true> {
+  using type = _Float16;
+};
+
 // 64-wide heads leave registers for two blocks a CU.
 template <typename T, bool F8, int DIM>
 __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(AttnArgs a, AttnPart part) {
   using R = Row<F8, DIM>;
   using x8 = typename Vec<T>::x8;
+  using W = typename WeightType<T, F8>::type;
+  using w8 = typename Vec<W>::x8;
   constexpr int BM = kWaves * 32, TILE = kBN * R::kBytes, KS = DIM / 16, DB = DIM / 32;
   constexpr int KR = F8 ? KS / 2 : KS;   // LDS reads of 32 positions' keys
   // Fragments read ahead of the products.  256-wide heads: three, four take registers that the addresses
@@ -129,7 +142,7 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
   // in LDS with its chunks permuted by `swizzle`, which is linear in the row's bits.
   const int grp = wave & 3;
   const bool values = wave >= 4;
-  using V = ValueReader<T, F8, DIM>;
+  using V = ValueReader<W, F8, DIM>;
   const uint32_t lds0 = lds_addr(lds);
   const int lrow = lane / R::kChunks, lslot = lane % R::kChunks;
   const uint32_t row_off = uint32_t(lrow) * uint32_t(a.c.token_stride);
@@ -181,7 +194,7 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[d][e] = 0;
   bool again = false;
-  const ValueReader<T, F8, DIM> vr(lane);
+  const ValueReader<W, F8, DIM> vr(lane);
   const uint32_t kbase = uint32_t(col * R::kBytes + ((hh ^ R::key_swizzle(col)) << 4));
 
   // S^T of 32 positions: fragments are read kAhead products before they are needed and no earlier, since
@@ -218,13 +231,13 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
     __builtin_amdgcn_s_setprio(0);
   };
   // Weights of the scores, after the running maximum moved on and outputs with it where it had to.
-  auto weights = [&](const f32x16& st, x8 (&w)[2]) {
+  auto weights = [&](const f32x16& st, w8 (&w)[2]) {
     float mx = st[0];
 #pragma unroll
     for (int e = 1; e < 16; ++e) mx = __builtin_fmaxf(mx, st[e]);
     mx = max_halves(mx) * c;
-    if (__any(ahead<T>(mx, top))) {
-      const float next = next_reference<T>(mx, top), keep = __builtin_amdgcn_exp2f(top - next);
+    if (__any(ahead<W>(mx, top))) {
+      const float next = next_reference<W>(mx, top), keep = __builtin_amdgcn_exp2f(top - next);
       top = next;
       sum *= keep;
 #pragma unroll
@@ -240,15 +253,15 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
       const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e + 1], c, -top));
       add += w0;
       add += w1;
-      // The weights' one rounding, to the type of the product: matrix units bound this kernel, and a second
+      // The weights' one rounding, to the type of the second product: matrix units bound this kernel, and a second
       // product with the remainders, as decoded rows have, takes 2,265 instead of 1,612 us at 16,002 rows.
-      pk[e >> 3][(e >> 1) & 3] = pack_pair<T>(w0, w1);
+      pk[e >> 3][(e >> 1) & 3] = pack_pair<W>(w0, w1);
     }
     sum += add;
-    w[0] = __builtin_bit_cast(x8, pk[0]);
-    w[1] = __builtin_bit_cast(x8, pk[1]);
+    w[0] = __builtin_bit_cast(w8, pk[0]);
+    w[1] = __builtin_bit_cast(w8, pk[1]);
   };
-  auto outputs = [&](uint32_t vt, const x8 (&w)[2], auto&& between) {
+  auto outputs = [&](uint32_t vt, const w8 (&w)[2], auto&& between) {
     uint32_t va = vt + vr.base;
     asm volatile("" : "+v"(va));   // the permuted addresses are made here, not kept
     // the n-th read's columns: as above, those 256 bytes apart follow each other
@@ -259,9 +272,9 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
     for (int n = 0; n < kAhead; ++n) f[n] = V::read(va, n & 1, col_of(n));
 #pragma unroll
     for (int n = 0; n < 2 * DB; ++n) {
-      const x8 vf = __builtin_bit_cast(x8, f[n % kAhead]);
+      const w8 vf = __builtin_bit_cast(w8, f[n % kAhead]);
       if (n + kAhead < 2 * DB) f[n % kAhead] = V::read(va, (n + kAhead) & 1, col_of(n + kAhead));
-      o[col_of(n)] = mfma32<T>(vf, w[n & 1], o[col_of(n)]);
+      o[col_of(n)] = mfma32<W>(vf, w[n & 1], o[col_of(n)]);
       between(n, 2 * DB);
     }
     sched_pipeline<kAhead, 2 * DB, 1, F8 ? 1 : 2>();
@@ -293,7 +306,7 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
       // exponentials (8,000 rows of 16 heads: 191 -> 186 us; wider heads gain nothing).
       if (DIM == 64 && wave >= 4) __builtin_amdgcn_s_sleep(2);
       f32x16 st;
-      x8 w[2];
+      w8 w[2];
       scores(kt, st, [&](int n, int of) {
 #pragma unroll
         for (int x = EARLY * n / of; x < EARLY * (n + 1) / of; ++x) load(it + 1, x);
@@ -342,7 +355,7 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
       if (p0 > tw_hi || (a.window >= 0 && p0 + 31 < loww && p0 >= a.sinks)) continue;
       const uint32_t kt = lds0 + buf * TILE + half * 32 * R::kBytes;
       f32x16 st;
-      x8 w[2];
+      w8 w[2];
       scores(kt, st, [](int, int) {});
       const uint32_t badp = (anybad >> (2 * half)) & 3u;
       // of a border step, a wave's rows often see all or nothing

@@ -1,5 +1,5 @@
 """How much of a weight survives the product with the values: weights far below the largest one, scores whose
-steps are wide, and decoded rows' weights past their first rounding.  The fp64 reference of
+steps are wide, decoded rows' weights past their first rounding, and prompts' over e4m3 pages.  The fp64 reference of
 tests/attn_util.py; bounds counted here."""
 import numpy as np
 import pytest
@@ -84,3 +84,12 @@ def test_decoded_rows_lose_no_weight_to_the_product_type(mass, rows, lens, heads
     y = ra.attn(c, b, p.q, window=window, sinks=sinks, mass_out=out)
     check_against(y, p.reference(window=window, sinks=sinks), dtype, dim, HALF_STEP[dtype] ** 2,
                   2.0 ** -36 if dtype == "f16" else 0.0)
+
+
+@pytest.mark.parametrize("rows,lens,heads,kv,dim,window,sinks", [
+    ([130], [517], 4, 1, 64, -1, 0), ([65, 1, 33], [65, 200, 300], 4, 2, 128, -1, 0), ([129], [700], 4, 1, 256, 129, 40)])
+def test_prompts_over_e4m3_pages_round_weights_to_fp16(rows, lens, heads, kv, dim, window, sinks):
+    p = Problem(19 + dim, rows, lens, heads, kv, dim, 48, "bf16", "e4m3")
+    c, b = p.make()
+    y = ra.attn(c, b, p.q, window=window, sinks=sinks)
+    check_against(y, p.reference(window=window, sinks=sinks), "bf16", dim, HALF_STEP["f16"], 2.0 ** -36)
