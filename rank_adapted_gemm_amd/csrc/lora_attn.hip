@@ -188,7 +188,7 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
   };
 
   f32x16 o[DB];
-  float top = kLowest, sum = 0;
+  float top = kLowest, sum = nan_scale(sc, units);
 #pragma unroll
   for (int d = 0; d < DB; ++d)
 #pragma unroll

@@ -42,6 +42,12 @@ __device__ __forceinline__ float next_reference(float mx, float ref) {
   return __builtin_fmaxf(ref, next);
 }
 
+// First value of a row's sum: NaN where scores are, as with a scale that is NaN and a row that sees a position.
+// (Kernels take the scale's magnitude from a maximum with the smallest number, which drops a NaN.)
+__device__ __forceinline__ float nan_scale(float scale, const Units& units) {
+  return scale != scale && units.count > 0 ? scale : 0.0f;
+}
+
 template <typename T>
 __device__ __forceinline__ f32x16 mfma32(typename Vec<T>::x8 a, typename Vec<T>::x8 b, f32x16 c) {
   if constexpr (__is_same(T, __bf16)) return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);

@@ -227,7 +227,7 @@ __global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16
 #pragma unroll
   for (int i = 0; i < QT; ++i) {
     top[i] = kLowest;
-    sum[i] = 0;
+    sum[i] = nan_scale(sc, units);
 #pragma unroll
     for (int d = 0; d < DB; ++d) o[i][d] = f32x4{0, 0, 0, 0};
   }
