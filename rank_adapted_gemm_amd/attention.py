@@ -22,6 +22,20 @@ KV_DTYPES = {"bf16": 0, "f16": 1, "e4m3": 2}
 MAX_KV_LEN, MAX_PAGE_SIZE, MAX_HEADS = 1 << 24, 65536, 512
 
 
+def _i32(x):
+    """x as the library's 32-bit integer.  The nearest one where x lies outside: it means the same there (no
+    limit, or too much), while ctypes would drop the upper bits."""
+    return max(-(1 << 31), min(int(x), (1 << 31) - 1))
+
+
+def _i32_array(name, values):
+    """Host int32 array of `values`, which have to fit."""
+    values = [int(x) for x in values]
+    if any(x != _i32(x) for x in values):
+        raise ValueError(f"{name} holds values past 32 bits")
+    return (ctypes.c_int32 * max(len(values), 1))(*values)
+
+
 def _strides3(name, t, dim):
     """Element strides of a (rows, heads, dim) tensor; a dimension of one element has no stride of its own."""
     shape, stride = t.shape, t.stride()
@@ -80,8 +94,7 @@ class KVBatch:
         self.kv_len = [int(x) for x in kv_len]
         self.max_len = max(self.kv_len, default=0)
         self._pages, self._index = page_table.shape[1], page_table.get_device()
-        self._starts = (ctypes.c_int32 * (n + 1))(*[int(x) for x in q_starts])
-        self._lens = (ctypes.c_int32 * max(n, 1))(*self.kv_len)
+        self._starts, self._lens = _i32_array("q_starts", q_starts), _i32_array("kv_len", self.kv_len)
         self._c = _bd.KVBatchStruct(ctypes.cast(self._starts, ctypes.c_void_p),
                                     ctypes.cast(self._lens, ctypes.c_void_p), page_table.data_ptr(), self.stride, n)
         self._ref = ctypes.byref(self._c)
@@ -165,7 +178,7 @@ def kv_append(cache, batch, k, v, stream=None):
 
 def attn_workspace_bytes(cache, batch, heads, window=-1, sinks=0, mass=False):
     """Bytes of scratch attn() needs for this batch."""
-    return int(_bd.load().lora_attn_workspace_bytes(cache._ref, batch._ref, int(heads), int(window), int(sinks),
+    return int(_bd.load().lora_attn_workspace_bytes(cache._ref, batch._ref, _i32(heads), _i32(window), _i32(sinks),
                                                     1 if mass else 0))
 
 
@@ -212,7 +225,7 @@ def attn(cache, batch, q, scale=None, window=-1, sinks=0, out=None, mass=None, m
     ws, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None \
         else (None, 0)
     _raise(_bd.load().lora_attn(cache._ref, batch._ref, q.data_ptr(), strides[0], strides[1], heads, code,
-                                cache.head_dim ** -0.5 if scale is None else float(scale), int(window), int(sinks),
+                                cache.head_dim ** -0.5 if scale is None else float(scale), _i32(window), _i32(sinks),
                                 out.data_ptr(), m_in, m_out, cap, ws, ws_bytes, s))
     return out
 
@@ -245,6 +258,6 @@ def kv_evict(cache, batch, mass, budget, dst_table, sinks=0, recent=0, kept=None
     if mass_out is None:
         mass_out = _empty(shape, torch.float32, dev, stream)
     m_out = _mass_ptr("mass_out", mass_out, shape, dev)
-    _raise(_bd.load().lora_kv_evict(cache._ref, batch._ref, m_in, cap, budget, int(sinks), int(recent),
+    _raise(_bd.load().lora_kv_evict(cache._ref, batch._ref, m_in, cap, _i32(budget), _i32(sinks), _i32(recent),
                                     dst_table.data_ptr(), dst_stride, kept.data_ptr(), m_out, s))
     return kept, mass_out
