@@ -157,7 +157,7 @@ struct Row {
 // Scalar view of an item's table row and pages.
 struct Pages {
   const int32_t* row;
-  int t_lo, t_hi, lo_pos;   // positions of the tile's rows; the first one in a window
+  int t_lo, t_hi, lo_pos;   // positions of the tile's rows; the first one in a window, 0 without one
   int window, sinks;
 
   // Some row of the tile sees a position of the 16-slot group at p0.
@@ -179,7 +179,7 @@ __device__ __forceinline__ Pages pages_of(const AttnArgs& a, int index, int t_lo
   p.t_hi = t_hi;
   p.window = a.window;
   p.sinks = a.sinks;
-  p.lo_pos = a.window == 0 ? 0x7FFFFFFF - 15 : (t_lo - a.window + 1 > 0 ? t_lo - a.window + 1 : 0);
+  p.lo_pos = a.window < 0 ? 0 : (a.window == 0 ? 0x7FFFFFFF - 15 : (t_lo - a.window + 1 > 0 ? t_lo - a.window + 1 : 0));
   return p;
 }
 

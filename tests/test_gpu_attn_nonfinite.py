@@ -1,0 +1,38 @@
+"""Infinite and NaN values at positions that rows see, wherever these lie in a kernel's step."""
+import numpy as np
+import pytest
+import torch
+
+import rank_adapted_gemm_amd as ra
+from attn_util import Problem, check_out, values
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("cache", [None, "e4m3"])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("back", [0, 1, 2, 5])
+@pytest.mark.parametrize("rows,length,window,sinks", [
+    (1, 200, -1, 0), (1, 21, -1, 0), (3, 90, -1, 0), (50, 180, -1, 0), (90, 90, -1, 0),
+    (1, 200, 40, 3), (3, 300, 64, 0), (60, 200, 30, 0)])
+def test_every_row_that_sees_a_value_gets_it(rows, length, window, sinks, back, value, cache):
+    """Counted back from the first row's own position."""
+    if cache and value == float("inf"):
+        pytest.skip("e4m3 has no infinity")
+    p = Problem(3, [rows], [length], 4, 2, 64, 16, cache=cache)
+    pos = length - rows - back
+    if pos < 0:
+        pytest.skip("before the first position")
+    ref = p.reference(window=window, sinks=sinks)
+    page, slot = int(p.table[0, pos // 16]), pos % 16
+    raw = p.v.view(torch.uint8) if cache else p.v
+    raw[page, slot, 0, 5] = 0x7F if cache else value
+    c, b = p.make()
+    y = values(ra.attn(c, b, p.q, window=window, sinks=sinks))
+    t = length - rows + np.arange(rows)
+    sees = (t >= pos) & ((window < 0) | (pos > t - window) | (pos < sinks))
+    hit = np.zeros(y.shape, dtype=bool)
+    hit[sees, :2, 5] = True                        # the heads of key-value head 0
+    assert (np.isnan(y[hit]) if np.isnan(value) else y[hit] == value).all()
+    y[hit] = ref["out"][hit]
+    check_out(torch.from_numpy(y), ref, "bf16", 64)
