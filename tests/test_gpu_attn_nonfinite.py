@@ -11,9 +11,9 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("cache", [None, "e4m3"])
 @pytest.mark.parametrize("value", [float("inf"), float("nan")])
-@pytest.mark.parametrize("back", [0, 1, 2, 5])
+@pytest.mark.parametrize("back", [0, 1, 2, 5, 20, 33, 70])
 @pytest.mark.parametrize("rows,length,window,sinks", [
-    (1, 200, -1, 0), (1, 21, -1, 0), (3, 90, -1, 0), (50, 180, -1, 0), (90, 90, -1, 0),
+    (1, 200, -1, 0), (1, 21, -1, 0), (3, 90, -1, 0), (1, 4000, -1, 0), (50, 180, -1, 0), (90, 90, -1, 0),
     (1, 200, 40, 3), (3, 300, 64, 0), (60, 200, 30, 0)])
 def test_every_row_that_sees_a_value_gets_it(rows, length, window, sinks, back, value, cache):
     """Counted back from the first row's own position."""
