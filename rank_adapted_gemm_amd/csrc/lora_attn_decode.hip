@@ -234,8 +234,9 @@ __global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16
   const ValueReader16<T, F8, DIM> vr(lane);
   const uint32_t kbase = uint32_t(col * R::kBytes + ((qd ^ R::key_swizzle(col)) << 4));
   float* scores = nullptr;
+  const int score_row = score_steps(units, sq.nsplit) * kStep;
   if constexpr (MASS)
-    scores = a.scores + (int64_t(blockIdx.x) * a.score_rows + col) * part.score_cols + qd * 4;
+    scores = a.scores + int64_t(sq.score) * kStep + ((int64_t(blockIdx.x) - first) * M + col) * score_row + qd * 4;
   bool again = false;
 
   for (int i = 0; i < mine; ++i) {
@@ -322,7 +323,7 @@ __global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16
         }
         if constexpr (MASS) {
           if (x * 16 + col < M)
-            *reinterpret_cast<f32x4*>(scores + int64_t(x) * 16 * part.score_cols + (wave + i * kWaves) * kStep + g * 16) = v;
+            *reinterpret_cast<f32x4*>(scores + int64_t(x) * 16 * score_row + (wave + i * kWaves) * kStep + g * 16) = v;
         }
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
@@ -595,11 +596,12 @@ __global__ __launch_bounds__(256) void decode_finish_kernel(AttnArgs a, AttnPart
     __syncthreads();
     if (met) {
       const int split = int((int64_t(u + 1) * sq.nsplit - 1) / units.count);
-      const float* sc = a.scores + (int64_t(first) + split * a.c.kv_heads + head) * a.score_rows * part.score_cols +
+      const int score_row = score_steps(units, sq.nsplit) * kStep;
+      const float* sc = a.scores + int64_t(sq.score) * kStep + (int64_t(split) * a.c.kv_heads + head) * M * score_row +
                         (u - split_begin(units.count, split, sq.nsplit)) * kStep + (p & (kStep - 1));
 #pragma unroll 4
       for (int m = 0; m < M; ++m) {
-        const float x = sc[int64_t(m) * part.score_cols];
+        const float x = sc[int64_t(m) * score_row];
         sum += x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(x - lse[m]);   // -inf: not seen
       }
     }

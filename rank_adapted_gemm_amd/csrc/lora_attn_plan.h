@@ -159,17 +159,15 @@ inline void attn_fill(AttnPath& path, AttnWork* w, int n, int chunk, const KvSeq
     AttnPart& p = path.part[path.parts];
     int& join = path.join_rows[path.parts];
     p.n = std::min(kAttnSeqs, n - at);
-    p.items = p.split_items = p.score_cols = p.mass_steps = join = 0;
+    p.items = p.split_items = p.mass_steps = join = 0;
     for (int i = 0; i < p.n; ++i) {
       const AttnWork& x = w[at + i];
       p.items += x.rows == 0 ? 0 : x.tiles * x.nsplit * kv_heads;
-      p.seq[i] = AttnSeq{s.q_start[x.index], x.rows, s.kv_len[x.index], p.items, x.nsplit, x.index};
+      p.seq[i] = AttnSeq{s.q_start[x.index], x.rows, s.kv_len[x.index], p.items, x.nsplit, x.index, 0};
       if (x.nsplit > 1) {
         p.split_items = p.items;
         join = std::max(join, (int(std::min<int64_t>(tile_rows, int64_t(x.rows) * group)) + x.nsplit - 1) / x.nsplit);
       }
-      if (x.rows > 0)
-        p.score_cols = std::max(p.score_cols, (x.units_last + x.nsplit - 1) / x.nsplit << kDecodeUnitShift);
     }
   }
 }
@@ -274,14 +272,22 @@ inline void attn_plan(AttnPlan& o, const KvView& c, const KvSeqs& s, int n_heads
 
   size_t rows_o = 0, rows_ml = 0, score = 0, arrived = 0, sums = 0;   // sums: of weights, after the joins
   for (int i = 0; i < o.decode.parts; ++i) {
-    const AttnPart& p = o.decode.part[i];
+    AttnPart& p = o.decode.part[i];
     rows_o = std::max(rows_o, size_t(p.split_items) * o.decode_tile);
     rows_ml = std::max(rows_ml, size_t(mass ? p.items : p.split_items) * o.decode_tile);
     o.inside[i] = !mass;
     for (int k = 0; k < p.n; ++k)
       if (int64_t(p.seq[k].rows) * group * p.seq[k].nsplit * c.dim * 4 > kJoinInside) o.inside[i] = false;
     if (o.inside[i]) arrived = std::max(arrived, size_t(p.split_items) * 8);
-    if (mass) score = std::max(score, size_t(p.items) * o.decode_rows * p.score_cols * 4);
+    if (!mass) continue;
+    size_t steps = 0;   // past 32 bits they are more than any workspace
+    for (int k = 0; k < p.n; ++k) {
+      AttnSeq& q = p.seq[k];
+      q.score = uint32_t(steps);
+      const Units u = units_of(q.kv_len - q.rows, q.kv_len - 1, window, sinks, kDecodeUnitShift);
+      if (q.rows > 0) steps += size_t(q.rows) * group * q.nsplit * c.kv_heads * score_steps(u, q.nsplit);
+    }
+    score = std::max(score, (steps << kDecodeUnitShift) * 4);
   }
   for (int i = 0; i < o.prompt.parts; ++i) {
     const AttnPart& p = o.prompt.part[i];

@@ -88,12 +88,12 @@ struct AttnSeq {
   int32_t item_end;              // items of this and all earlier sequences
   int32_t nsplit;
   int32_t index;                 // the sequence's number in the batch
+  uint32_t score;                // decode: where its items' scores start in the workspace, in steps of positions
 };
 
 struct AttnPart {
   int32_t n;
   int32_t items, split_items;    // items of sequences with nsplit > 1 come first
-  int32_t score_cols;            // decode: positions of an item's score rows in the workspace
   int32_t mass_steps;            // prompts' weights: steps of rows an item takes at most
   AttnSeq seq[kAttnSeqs];
 };
@@ -142,17 +142,23 @@ struct AttnArgs {
   float* lse;            // workspace: per (row, head), base 2 (prompts with accumulated weights), or NULL
   float* part_o;         // workspace: unnormalised output rows of split items
   float* part_ml;        // workspace: their maximum and sum
-  float* scores;         // workspace: scaled scores of decode items (accumulated weights), or NULL
+  float* scores;         // workspace: scaled scores of decode items (accumulated weights), or NULL; an item's
+                         // block holds its rows side by side, score_steps() steps of positions each
   uint64_t* arrived;     // workspace: decode items that are done, or NULL where a launch of its own joins them
   uint64_t call;         // this call's number, which `arrived` holds for them
   int64_t q_row_stride;  // bytes
   int64_t mass_cap;
   int32_t q_head_stride; // bytes
   int32_t heads, group;  // query heads; query heads per key-value head
-  int32_t score_rows;    // rows of a decode item's score block
   int32_t window, sinks;
   float scale;
 };
+
+// A launch's table travels as kernel arguments, of which there are 4 KiB.
+static_assert(sizeof(AttnArgs) + sizeof(AttnPart) <= 4096, "kernel arguments");
+
+// Steps of positions that a decode item's score rows hold: the longest split's.
+__host__ __device__ inline int score_steps(const Units& u, int nsplit) { return (u.count + nsplit - 1) / nsplit; }
 
 // Rows of a step of the prompts' weight kernel.
 __host__ __device__ constexpr int mass_step_rows(int dim) { return dim == 256 ? 64 : 128; }

@@ -236,7 +236,6 @@ lora_status lora_attn(const lora_kv_cache* cache, const lora_kv_batch* batch,
   a.mass_cap = mass_cap;
   a.heads = n_heads;
   a.group = n_heads / a.c.kv_heads;
-  a.score_rows = plan.decode_rows;
   a.window = window;
   a.sinks = sinks;
   a.scale = scale;
