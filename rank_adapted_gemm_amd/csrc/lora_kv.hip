@@ -376,11 +376,13 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_long_kernel(EvictArg
 
 constexpr int kGatherRows = 64;
 
-// Copies kept rows to their new slots, and their weights; blockIdx.y is (sequence, head).  Bound by bytes:
+// Copies kept rows to their new slots, and their weights; blockIdx.y is the head, z the sequence (their
+// product may pass 65,535, which a dimension of a grid is documented to hold).  Bound by bytes:
 // 101 MB of 512-byte rows in 17 us (5.8 TB/s), 786 MB of 128-byte rows in 160 us (4.9 TB/s).
 __global__ __launch_bounds__(256) void evict_gather_kernel(EvictArgs a, int elem_bytes, uint32_t nan_word) {
   __shared__ int64_t src[kGatherRows], dst[kGatherRows];   // byte offsets; -1: no row, -2: source page invalid
-  const int i = blockIdx.y / a.c.kv_heads, h = blockIdx.y - i * a.c.kv_heads;
+  const int i = blockIdx.z, h = blockIdx.y;
+  const int64_t pair = int64_t(i) * a.c.kv_heads + h;
   const int n = min(a.s.kv_len[i], a.budget);
   const int s0 = blockIdx.x * kGatherRows;
   if (s0 >= n) return;
@@ -388,7 +390,7 @@ __global__ __launch_bounds__(256) void evict_gather_kernel(EvictArgs a, int elem
     const int slot = s0 + threadIdx.x;
     int64_t so = -1, to = -1;
     if (slot < n) {
-      const int pos = a.kept[int64_t(blockIdx.y) * a.budget + slot];
+      const int pos = a.kept[pair * a.budget + slot];
       const int ss = pos >> 4, sp = page_of(a.c, ss), ds = slot >> 4, dp = page_of(a.c, ds);
       const int spage = a.s.table[i * a.s.table_stride + sp];
       const int dpage = a.dst_table[i * a.dst_stride + dp];
@@ -402,8 +404,8 @@ __global__ __launch_bounds__(256) void evict_gather_kernel(EvictArgs a, int elem
     src[threadIdx.x] = so;
     dst[threadIdx.x] = to;
     if (slot < n && a.mass_out && a.s.kv_len[i] > a.budget)   // a sequence kept whole has them already
-      a.mass_out[int64_t(blockIdx.y) * a.budget + slot] =
-          a.mass[int64_t(blockIdx.y) * a.mass_cap + a.kept[int64_t(blockIdx.y) * a.budget + slot]];
+      a.mass_out[pair * a.budget + slot] =
+          a.mass[pair * a.mass_cap + a.kept[pair * a.budget + slot]];
   }
   __syncthreads();
   const int per = a.c.dim * elem_bytes / 16;
@@ -452,8 +454,8 @@ hipError_t launch_kv_evict(const EvictArgs& a, int cache_dtype, hipStream_t stre
   }
   if (kept == 0) return hipSuccess;
   const bool f8 = cache_dtype == LORA_KV_E4M3;
-  hipLaunchKernelGGL(evict_gather_kernel, dim3((kept + kGatherRows - 1) / kGatherRows, pairs), dim3(256), 0, stream, a,
-                     f8 ? 1 : 2, f8 ? 0x7F7F7F7Fu : 0x7FFF7FFFu);
+  hipLaunchKernelGGL(evict_gather_kernel, dim3((kept + kGatherRows - 1) / kGatherRows, a.c.kv_heads, a.s.n), dim3(256), 0,
+                     stream, a, f8 ? 1 : 2, f8 ? 0x7F7F7F7Fu : 0x7FFF7FFFu);
   return hipGetLastError();
 }
 
