@@ -59,10 +59,11 @@
  * the arguments alone: no order of arrival enters them.
  *
  * Streams, ownership and errors are lora_proj.h's: calls are asynchronous on
- * `stream`, check every host argument before the first launch, allocate
- * nothing, keep nothing between calls, and return LORA_EHIP when a launch
- * fails.  HOST arrays and the two structs may be released when the call
- * returns.  A batch without rows (append, attn) or sequences is a no-op.
+ * `stream`, check every host argument before the first launch, allocate nothing,
+ * keep nothing between calls, and return LORA_EHIP when a launch fails.  The
+ * stream and all device pointers belong to the current device.  HOST arrays and
+ * the two structs may be released when the call returns.  A batch without rows
+ * (append, attn) or sequences is a no-op.
  */
 #ifndef LORA_ATTN_H
 #define LORA_ATTN_H

@@ -158,7 +158,19 @@ def _mass_ptr(name, t, shape, dev):
     return t.data_ptr()
 
 
-def _raise(status):
+def _current_gpu():
+    import torch
+    return torch.cuda.current_device()
+
+
+def _call(cache, entry, *args):
+    """entry(*args) with the cache's GPU current, which is where the library launches; raises on a status."""
+    if _current_gpu() == cache._index:
+        status = entry(*args)
+    else:
+        import torch
+        with torch.cuda.device(cache._index):
+            status = entry(*args)
     if status != _bd.LORA_OK:
         raise _bd.LoraError(status, _bd.status_string(status))
 
@@ -172,8 +184,8 @@ def kv_append(cache, batch, k, v, stream=None):
     if code != _row_code(cache, batch, "v", v) or k.shape != v.shape or k.shape[1] != cache.kv_heads or \
             strides != _strides3("v", v, cache.head_dim):
         raise ValueError("k and v must be (rows, kv_heads, head_dim) of one type and the same strides")
-    _raise(_bd.load().lora_kv_append(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), strides[0], strides[1],
-                                     code, _handle(stream, cache)))
+    _call(cache, _bd.load().lora_kv_append, cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), strides[0], strides[1],
+          code, _handle(stream, cache))
 
 
 def attn_workspace_bytes(cache, batch, heads, window=-1, sinks=0, mass=False):
@@ -224,9 +236,9 @@ def attn(cache, batch, q, scale=None, window=-1, sinks=0, out=None, mass=None, m
         raise ValueError(f"workspace must be a contiguous CUDA tensor on {dev}")
     ws, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None \
         else (None, 0)
-    _raise(_bd.load().lora_attn(cache._ref, batch._ref, q.data_ptr(), strides[0], strides[1], heads, code,
-                                cache.head_dim ** -0.5 if scale is None else float(scale), _i32(window), _i32(sinks),
-                                out.data_ptr(), m_in, m_out, cap, ws, ws_bytes, s))
+    _call(cache, _bd.load().lora_attn, cache._ref, batch._ref, q.data_ptr(), strides[0], strides[1], heads, code,
+          cache.head_dim ** -0.5 if scale is None else float(scale), _i32(window), _i32(sinks),
+          out.data_ptr(), m_in, m_out, cap, ws, ws_bytes, s)
     return out
 
 
@@ -258,6 +270,6 @@ def kv_evict(cache, batch, mass, budget, dst_table, sinks=0, recent=0, kept=None
     if mass_out is None:
         mass_out = _empty(shape, torch.float32, dev, stream)
     m_out = _mass_ptr("mass_out", mass_out, shape, dev)
-    _raise(_bd.load().lora_kv_evict(cache._ref, batch._ref, m_in, cap, _i32(budget), _i32(sinks), _i32(recent),
-                                    dst_table.data_ptr(), dst_stride, kept.data_ptr(), m_out, s))
+    _call(cache, _bd.load().lora_kv_evict, cache._ref, batch._ref, m_in, cap, _i32(budget), _i32(sinks), _i32(recent),
+          dst_table.data_ptr(), dst_stride, kept.data_ptr(), m_out, s)
     return kept, mass_out

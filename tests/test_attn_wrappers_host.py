@@ -25,6 +25,7 @@ def setup(monkeypatch):
     lib = Library()
     monkeypatch.setattr(bd, "_lib", lib)
     monkeypatch.setattr(at, "_handle", lambda stream, cache: 0)
+    monkeypatch.setattr(at, "_current_gpu", lambda: -1, raising=False)   # where the stand-in's cache lies
     monkeypatch.setattr(at, "_table", lambda name, t, n, torch: (t, t.shape[1]))
     cache = SimpleNamespace(_index=-1, device=torch.device("cpu"), page_size=16, kv_heads=2, head_dim=64,
                             _row_codes={torch.bfloat16: 0}, _ref=None)
@@ -54,3 +55,30 @@ def test_counts_of_an_eviction_past_32_bits_stay_too_large(setup):
 def test_batches_past_32_bits_are_refused(setup, q_starts, kv_len):
     with pytest.raises(ValueError, match="32 bits"):
         at.KVBatch(q_starts, kv_len, torch.zeros(len(kv_len), 2, dtype=torch.int32))
+
+
+def test_calls_run_with_the_caches_gpu_current(setup, monkeypatch):
+    """The library launches on the current GPU, which need not be the cache's."""
+    lib, cache, batch = setup
+    current = [1]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    seen = []
+    monkeypatch.setattr(at, "_current_gpu", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(Library, "__getattr__", lambda self, name: lambda *a: (seen.append((name, current[0])), 0)[1])
+    q, mass, dst = torch.zeros(1, 4, 64, dtype=torch.bfloat16), torch.zeros(1, 2, 20), torch.zeros(1, 2, dtype=torch.int32)
+    at.attn(cache, batch, q, out=torch.empty_like(q), workspace=torch.zeros(16))
+    at.kv_append(cache, batch, q[:, :2], q[:, 2:])
+    at.kv_evict(cache, batch, mass, 8, dst)
+    assert seen == [("lora_attn", -1), ("lora_kv_append", -1), ("lora_kv_evict", -1)]
+    assert current == [1]
