@@ -151,6 +151,24 @@ size_t lora_attn_workspace_bytes(const lora_kv_cache* cache, const lora_kv_batch
                                  int32_t window, int32_t sinks, int32_t with_mass);
 
 /*
+ * lora_attn_plan_describe — how lora_attn would cut the call into launches, for inspection and
+ * host-side tests; nothing is launched.
+ *
+ *   out   HOST, receives up to n_out values, LORA_ATTN_PLAN_VALUES for each launch of a row kernel,
+ *         decoded sequences' first:
+ *     prompt        0 for the decode kernel, 1 for the prompts'
+ *     sequences     in the launch's table
+ *     items         blocks
+ *     split_items   of those, blocks that share their rows with others and leave sums
+ *     joined        1 where the last of a row's items joins it, 0 where a launch does (or nothing is split)
+ *
+ * Returns the number of launches, or 0 for arguments lora_attn would reject or without work.
+ */
+#define LORA_ATTN_PLAN_VALUES 5
+int32_t lora_attn_plan_describe(const lora_kv_cache* cache, const lora_kv_batch* batch, int32_t n_heads,
+                                int32_t window, int32_t sinks, int32_t with_mass, int64_t* out, int32_t n_out);
+
+/*
  * lora_kv_evict — bring every sequence down to `budget` positions per key-value head.
  *
  * Of a sequence of L > budget positions each head keeps the first `sinks`, the last `recent`

@@ -5,7 +5,7 @@ Y = X W^T on all other rows, computed by hand-written HIP kernels behind the
 C-ABI declared in include/lora_proj.h.  Importing the package loads nothing;
 the first call loads liblora_proj.so and fails if it is not built.
 """
-from .attention import (KVBatch, KVCache, attn, attn_workspace, attn_workspace_bytes, kv_append,  # noqa: F401
-                        kv_evict)
+from .attention import (KVBatch, KVCache, attn, attn_plan, attn_workspace, attn_workspace_bytes,  # noqa: F401
+                        kv_append, kv_evict)
 from .binding import (LoraError, lora_proj, lora_proj_raw, path, status_string,  # noqa: F401
                       workspace_bytes, load)

@@ -194,6 +194,15 @@ def attn_workspace_bytes(cache, batch, heads, window=-1, sinks=0, mass=False):
                                                     1 if mass else 0))
 
 
+def attn_plan(cache, batch, heads, window=-1, sinks=0, mass=False):
+    """How attn() cuts a call into launches (lora_attn_plan_describe): a dict a launch, for inspection."""
+    n = len(_bd.ATTN_PLAN_FIELDS)
+    out = (ctypes.c_int64 * (4 * n))()
+    launches = _bd.load().lora_attn_plan_describe(cache._ref, batch._ref, _i32(heads), _i32(window), _i32(sinks),
+                                                  1 if mass else 0, out, 4 * n)
+    return [dict(zip(_bd.ATTN_PLAN_FIELDS, out[i * n:(i + 1) * n])) for i in range(launches)]
+
+
 def attn_workspace(cache, batch, heads, window=-1, sinks=0, mass=False, stream=None):
     """A workspace tensor for attn() with these arguments (None when it needs none).  One workspace serves
     every layer of a step, in order on one stream."""

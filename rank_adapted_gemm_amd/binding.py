@@ -27,10 +27,11 @@ EXPORTS = ("lora_proj", "lora_proj_ex", "lora_proj_multi", "lora_proj_sliced", "
            "lora_proj_path", "lora_proj_tile_rows", "lora_status_string", "lora_extract", "lora_extract_workspace_bytes",
            "lora_probe_mfma_bf16", "lora_probe_read", "lora_workspace_status", "lora_debug_handover_fault",
            "lora_decode_plan_describe", "lora_proj_noalloc", "lora_proj_ranked", "lora_kv_append", "lora_attn",
-           "lora_attn_workspace_bytes", "lora_kv_evict")
+           "lora_attn_workspace_bytes", "lora_attn_plan_describe", "lora_kv_evict")
 NOALLOC_SCRATCH_BYTES = 64 << 20   # the device array lora_proj_noalloc uses instead of a workspace
 PLAN_FIELDS = ("MT", "nst", "nrs", "ntA", "ntW", "n_used", "GA", "GW", "smaxW", "off_cnt", "off_pa", "pa_bytes",
                "off_pw", "pw_bytes", "off_th", "t_bytes", "off_tl", "total")
+ATTN_PLAN_FIELDS = ("prompt", "sequences", "items", "split_items", "joined")
 
 _lib = None
 
@@ -121,6 +122,8 @@ def load():
     lib.lora_attn.restype = ctypes.c_int
     lib.lora_attn_workspace_bytes.argtypes = [vp, vp, i32, i32, i32, i32]
     lib.lora_attn_workspace_bytes.restype = sz
+    lib.lora_attn_plan_describe.argtypes = [vp, vp, i32, i32, i32, i32, ctypes.POINTER(i64), i32]
+    lib.lora_attn_plan_describe.restype = i32
     lib.lora_kv_evict.argtypes = [vp, vp, vp, i64, i32, i32, i32, vp, i64, vp, vp, vp]
     lib.lora_kv_evict.restype = ctypes.c_int
     _lib = lib

@@ -119,6 +119,20 @@ lora_status check_heads(const KvView& c, const KvSeqs& s, int32_t n_heads) {
   return LORA_OK;
 }
 
+// The plan of a call; false for arguments lora_attn would reject or without work.
+bool plan_of(const lora_kv_cache* cache, const lora_kv_batch* batch, int32_t n_heads, int32_t window, int32_t sinks,
+             int32_t with_mass, lora::AttnPlan& plan) {
+  KvView c;
+  KvSeqs s;
+  size_t pool = 0;
+  if (check_cache(cache, c, pool) != LORA_OK || check_batch(batch, cache->page_size, true, s) != LORA_OK ||
+      check_heads(c, s, n_heads) != LORA_OK || sinks < 0)
+    return false;
+  if (s.n == 0 || (s.q_start[s.n] == 0 && !with_mass)) return false;
+  lora::attn_plan(plan, c, s, n_heads, window, sinks, with_mass != 0, int(elem_bytes(cache->dtype)));
+  return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -149,16 +163,28 @@ lora_status lora_kv_append(const lora_kv_cache* cache, const lora_kv_batch* batc
 
 size_t lora_attn_workspace_bytes(const lora_kv_cache* cache, const lora_kv_batch* batch, int32_t n_heads,
                                  int32_t window, int32_t sinks, int32_t with_mass) {
-  KvView c;
-  KvSeqs s;
-  size_t pool = 0;
-  if (check_cache(cache, c, pool) != LORA_OK || check_batch(batch, cache->page_size, true, s) != LORA_OK ||
-      check_heads(c, s, n_heads) != LORA_OK || sinks < 0)
-    return 0;
-  if (s.n == 0 || (s.q_start[s.n] == 0 && !with_mass)) return 0;
   lora::AttnPlan plan;
-  lora::attn_plan(plan, c, s, n_heads, window, sinks, with_mass != 0, int(elem_bytes(cache->dtype)));
-  return plan.bytes;
+  return plan_of(cache, batch, n_heads, window, sinks, with_mass, plan) ? plan.bytes : 0;
+}
+
+int32_t lora_attn_plan_describe(const lora_kv_cache* cache, const lora_kv_batch* batch, int32_t n_heads,
+                                int32_t window, int32_t sinks, int32_t with_mass, int64_t* out, int32_t n_out) {
+  lora::AttnPlan plan;
+  if (!out || !plan_of(cache, batch, n_heads, window, sinks, with_mass, plan)) return 0;
+  int32_t n = 0, launches = 0;
+  for (int prompt = 0; prompt < 2; ++prompt) {
+    const lora::AttnPath& path = prompt ? plan.prompt : plan.decode;
+    for (int i = 0; i < path.parts; ++i) {
+      const lora::AttnPart& p = path.part[i];
+      if (p.items == 0) continue;   // sequences without rows, whose weights are carried over
+      const int64_t v[LORA_ATTN_PLAN_VALUES] = {prompt, p.n, p.items, p.split_items,
+                                                !prompt && plan.inside[i] && p.split_items > 0};
+      for (int64_t x : v)
+        if (n < n_out) out[n++] = x;
+      ++launches;
+    }
+  }
+  return launches;
 }
 
 lora_status lora_attn(const lora_kv_cache* cache, const lora_kv_batch* batch,

@@ -5,16 +5,31 @@ import pytest
 
 from rank_adapted_gemm_amd import binding as bd
 from test_attn_host import batch, cache
+from test_gpu_attn_many import SHAPES
 
 
-def query(rows, lens, heads, kv_heads, dim, mass, window=-1, sinks=0, page=64):
+def structs(rows, lens, kv_heads, dim, page=64):
     starts = [0]
     for n in rows:
         starts.append(starts[-1] + n)
     c = cache(n_pages=1 << 20, page_size=page, n_kv_heads=kv_heads, head_dim=dim, head_stride=dim, token_stride=kv_heads * dim,
               page_stride=page * kv_heads * dim)
     b = batch(starts, lens, table_stride=max(lens) // page + 1, n_seq=len(lens))
-    return bd.load().lora_attn_workspace_bytes(ctypes.byref(c), ctypes.byref(b), heads, window, sinks, mass)
+    return c, b
+
+
+def query(rows, lens, heads, kv_heads, dim, mass):
+    c, b = structs(rows, lens, kv_heads, dim)
+    return bd.load().lora_attn_workspace_bytes(ctypes.byref(c), ctypes.byref(b), heads, -1, 0, mass)
+
+
+def plan(rows, lens, heads, kv_heads, dim, mass=0, n_out=20):
+    """Launches of a call: (prompt, sequences, items, split items, joined) each."""
+    c, b = structs(rows, lens, kv_heads, dim)
+    out = (ctypes.c_int64 * 21)(*[-9] * 21)
+    n = bd.load().lora_attn_plan_describe(ctypes.byref(c), ctypes.byref(b), heads, -1, 0, mass, out, n_out)
+    assert list(out[n_out:]) == [-9] * (21 - n_out)
+    return [tuple(out[i * 5:i * 5 + 5]) for i in range(n)]
 
 
 @pytest.mark.parametrize("rows,lens,heads,kv_heads,dim", [
@@ -34,3 +49,24 @@ def test_scores_take_what_their_own_sequences_need(rows, lens, heads, kv_heads, 
     steps = sum((length + 31) // 32 * kv_heads for length in lens)
     extra = query(rows, lens, heads, kv_heads, dim, 1) - query(rows, lens, heads, kv_heads, dim, 0)
     assert extra <= 2 * scores + steps * 32 * 8 + 1024
+
+
+@pytest.mark.parametrize("mass", [0, 1])
+@pytest.mark.parametrize("name,prompt,split", [("decoded, the first launch split", 0, [True, False]),
+                                               ("decoded, both launches split", 0, [True, True]),
+                                               ("prompts, both launches split", 1, [True, True])])
+def test_large_batches_take_the_launches_their_gpu_test_is_for(name, prompt, split, mass):
+    rows, lens, heads, dim = SHAPES[name]
+    launches = plan(rows, lens, heads, 1, dim, mass)
+    assert [x[0] for x in launches] == [prompt, prompt] and sum(x[1] for x in launches) == len(rows)
+    assert launches[0][1] == 128                     # a full table
+    assert [x[3] > 0 for x in launches] == split
+    assert all(x[4] == (0 if prompt or mass else int(x[3] > 0)) for x in launches)
+
+
+def test_plans_of_no_work_and_short_buffers():
+    assert plan([0, 0], [20, 5], 4, 2, 64) == [] and plan([0, 0], [20, 5], 4, 2, 64, mass=1) == []
+    assert plan([1], [20], 5, 2, 64) == []           # heads that are no multiple
+    whole = plan([1, 90], [20, 90], 4, 2, 64)
+    assert whole == [(1, 2, 4, 0, 0)]                # a short sequence rides in the prompts' launch
+    assert plan([1, 90], [20, 90], 4, 2, 64, n_out=3) == [(1, 2, 4, -9, -9)]
