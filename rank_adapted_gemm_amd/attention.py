@@ -19,7 +19,6 @@ import ctypes
 from . import binding as _bd
 
 KV_DTYPES = {"bf16": 0, "f16": 1, "e4m3": 2}
-MAX_KV_LEN, MAX_PAGE_SIZE, MAX_HEADS = 1 << 24, 65536, 512
 
 
 def _i32(x):

@@ -6,13 +6,11 @@
 namespace lora {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 template <typename T>
 struct Vec {
   typedef T x2 __attribute__((ext_vector_type(2)));
-  typedef T x4 __attribute__((ext_vector_type(4)));
   typedef T x8 __attribute__((ext_vector_type(8)));
 };
 
@@ -157,7 +155,7 @@ struct Row {
 // Scalar view of an item's table row and pages.
 struct Pages {
   const int32_t* row;
-  int t_lo, t_hi, lo_pos;   // positions of the tile's rows; the first one in a window, 0 without one
+  int t_hi, lo_pos;         // position of the tile's last row; the first one in a window, 0 without one
   int window, sinks;
 
   // Some row of the tile sees a position of the 16-slot group at p0.
@@ -175,7 +173,6 @@ struct Pages {
 __device__ __forceinline__ Pages pages_of(const AttnArgs& a, int index, int t_lo, int t_hi) {
   Pages p;
   p.row = a.table + index * a.table_stride;
-  p.t_lo = t_lo;
   p.t_hi = t_hi;
   p.window = a.window;
   p.sinks = a.sinks;

@@ -6,9 +6,6 @@
 
 namespace lora {
 
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-
 // The cache as kernels see it: strides in bytes.
 struct KvView {
   char* k;
@@ -185,7 +182,6 @@ __host__ __device__ inline int mass_splits(RowRange r, int group, int step_rows,
 // Shapes of the two attention kernels.
 constexpr int kDecodeUnitShift = 5;   // 32 positions, one wave's step
 constexpr int kPromptUnitShift = 6;   // 64 positions, one block's step
-constexpr int kAttnDecodeRows = 16;       // packed rows a decode tile holds for each 16-row column of the product
 constexpr int kAttnDecodeMaxRows = 32;    // sequences of at most that many packed rows are decoded
 constexpr int kDecodeWaves = 4;
 constexpr int kPromptRows = 256;      // packed rows of a prompt tile
