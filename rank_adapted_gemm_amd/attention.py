@@ -159,7 +159,7 @@ def _mass_ptr(name, t, shape, dev):
 
 def _current_gpu():
     import torch
-    return torch.cuda.current_device()
+    return torch._C._cuda_getDevice()
 
 
 def _call(cache, entry, *args):
