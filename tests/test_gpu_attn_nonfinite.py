@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import rank_adapted_gemm_amd as ra
-from attn_util import Problem, check_out, values
+from attn_util import Problem, check_out, values, weight_error
 
 pytestmark = pytest.mark.gpu
 
@@ -28,7 +28,12 @@ def test_every_row_that_sees_a_value_gets_it(rows, length, window, sinks, back, 
     raw = p.v.view(torch.uint8) if cache else p.v
     raw[page, slot, 0, 5] = 0x7F if cache else value
     c, b = p.make()
+    mass = torch.zeros(1, 2, length, device="cuda")
     y = values(ra.attn(c, b, p.q, window=window, sinks=sinks))
+    assert np.array_equal(y, values(ra.attn(c, b, p.q, window=window, sinks=sinks, mass_out=mass)), equal_nan=True)
+    # the weights do not depend on values: their fp32 error, a rounding a term and the total's
+    got, want = values(mass)[0], ref["mass"][0]
+    assert (np.abs(got - want) <= (float(np.max(weight_error(ref, 64))) + (2 * rows + 2) * 2.0 ** -24) * want).all()
     t = length - rows + np.arange(rows)
     sees = (t >= pos) & ((window < 0) | (pos > t - window) | (pos < sinks))
     hit = np.zeros(y.shape, dtype=bool)
