@@ -70,3 +70,11 @@ def test_plans_of_no_work_and_short_buffers():
     whole = plan([1, 90], [20, 90], 4, 2, 64)
     assert whole == [(1, 2, 4, 0, 0)]                # a short sequence rides in the prompts' launch
     assert plan([1, 90], [20, 90], 4, 2, 64, n_out=3) == [(1, 2, 4, -9, -9)]
+
+
+def test_short_sequences_ride_beside_prompts_and_long_ones_do_not():
+    """A ride takes a step of the prompts' kernel for 64 positions whatever the width: six a CU are the limit."""
+    assert [x[0] for x in plan([482] + [1] * 6, [4002] + [200] * 6, 32, 8, 128)] == [1]
+    assert [x[0] for x in plan([482] + [1] * 12, [4002] + [940] * 12, 32, 8, 128)] == [1]       # 1,440 steps
+    assert [x[0] for x in plan([482] + [1] * 13, [4002] + [960] * 13, 32, 8, 128)] == [0, 1]    # 1,560
+    assert [x[0] for x in plan([482] + [1] * 12, [4002] + [7000] * 12, 32, 8, 128)] == [0, 1]
