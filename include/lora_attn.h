@@ -51,11 +51,11 @@
  *
  * Limits (LORA_EUNSUPPORTED beyond): head_dim 64, 128 or 256; page_size a
  * multiple of 16 up to 65536; n_seq <= LORA_MAX_SEGMENTS; kv_len <= 2^24;
- * n_heads <= 512; rows <= 2^24 and rows * n_heads < 2^31.
+ * n_heads and n_kv_heads <= 512; rows <= 2^24 and rows * n_heads < 2^31.
  *
  * How a call runs.  Sequences of at most 32 packed rows (rows times heads that share a key-value
  * head) are decoded; the rest are prompts, and a few short sequences beside them ride in their
- * launch.  Long caches are split over blocks, whose sums meet in the workspace.  Results depend on
+ * launch, as prompts.  Long caches are split over blocks, whose sums meet in the workspace.  Results depend on
  * the arguments alone: no order of arrival enters them.
  *
  * Streams, ownership and errors are lora_proj.h's: calls are asynchronous on
@@ -176,7 +176,9 @@ int32_t lora_attn_plan_describe(const lora_kv_cache* cache, const lora_kv_batch*
  * position; NaN ranks below everything); of L <= budget it keeps all.  The kept rows, in their
  * order, are copied from the pages of batch->page_table to slots 0, 1, ... of the pages of
  * dst_table.  Heads keep different positions, the same number of them: the sequence's new
- * length is min(L, budget).  The caller then frees the old pages.
+ * length is min(L, budget).  The caller then frees the old pages.  A position is from then on
+ * the number of its slot: a later `window` or `sinks` counts kept slots, not the tokens that
+ * were there, and `kept` alone says which these were.
  *
  *   mass        device fp32, (n_seq, n_kv_heads, mass_cap) as lora_attn accumulates it
  *   dst_table   device, n_seq rows of dst_stride entries, dst_stride at least

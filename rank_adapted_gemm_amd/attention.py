@@ -256,7 +256,7 @@ def kv_evict(cache, batch, mass, budget, dst_table, sinks=0, recent=0, kept=None
 
     ``mass`` (n_seq, kv_heads, cap) float32 is what attn() accumulated.  Returns (kept, mass_out): the kept
     positions (n_seq, kv_heads, budget) int32, then -1, and their mass, then 0.  Sequence i's new length is
-    min(kv_len[i], budget)."""
+    min(kv_len[i], budget), and its positions are slots from then on: a later window counts those."""
     import torch
     dev = cache.device
     _check_batch(cache, batch)
