@@ -17,10 +17,11 @@
 // of four waves too: 644 against 541 us for 8,000 rows of 32 heads of 128.
 //
 // Bound by the matrix unit and the power that it draws.  16,002 rows, 16 heads of
-// 256 over 4: 1.65 ms, 1.27 PFLOP/s (a large library product on the same card:
-// 1.35), matrix units busy for 66% of the cycles at 1.69 GHz, no LDS conflicts.
-// 8,000 rows of 32 heads of 128: 477 us, 1.10 PFLOP/s.  At 64-wide heads the
-// exponentials are the larger part: 8,000 rows of 16 heads, 186 us, 0.70 PFLOP/s.
+// 256 over 4: 1.61 - 1.73 ms from card to card, 1.22 - 1.30 PFLOP/s (a large library
+// product: 1.35), under a window of 4,096 matrix units busy for 55% of the cycles at
+// 1.84 GHz, no LDS conflicts.  8,000 rows of 32 heads of 128: 474 - 500 us, 1.05 -
+// 1.10 PFLOP/s.  At 64-wide heads the exponentials are the larger part: 8,000 rows
+// of 16 heads, 177 - 184 us, 0.71 - 0.74 PFLOP/s.
 #include "lora_attn_core.h"
 
 namespace lora {
@@ -94,8 +95,8 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
   constexpr int BM = kWaves * 32, TILE = kBN * R::kBytes, KS = DIM / 16, DB = DIM / 32;
   constexpr int KR = F8 ? KS / 2 : KS;   // LDS reads of 32 positions' keys
   // Fragments read ahead of the products.  256-wide heads: three, four take registers that the addresses
-  // need (a 4,096 window over 16,002 rows: 842 against 862 us); narrower ones: four (128-wide e4m3 prompt of
-  // 8,000 rows: 505 against 512 us).
+  // need (a 4,096 window over 16,002 rows: 854 against 868 us); narrower ones: four (8,000 rows of 32 heads of
+  // 128 over e4m3 pages: 523 against 526 us with three, though 495 against 489 over bf16 ones).
   constexpr int kAhead = DIM == 256 ? 3 : 4;
   static_assert(BM == kPromptRows, "one tile height for the host's plan");
   __shared__ __attribute__((aligned(1024))) char lds[4 * TILE];   // keys, keys, values, values
@@ -303,7 +304,7 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
       aim(it + 1);
       // Waves w and w + 4 share a SIMD and leave the barrier together.  At 64-wide heads, where a step is
       // short and mostly exponentials, 128 cycles' delay of one lets its products run beside the other's
-      // exponentials (8,000 rows of 16 heads: 191 -> 186 us; wider heads gain nothing).
+      // exponentials (300 rows of 8 heads: 11.2 -> 11.0 us, 8,000 of 16 the same; wider heads gain nothing).
       if (DIM == 64 && wave >= 4) __builtin_amdgcn_s_sleep(2);
       f32x16 st;
       w8 w[2];

@@ -13,10 +13,11 @@
 // O^T = V^T P^T run on 16 x 16 x 32 MFMAs as in the prompts' kernel.  The waves
 // join in LDS; items that share rows leave sums in the workspace for the join.
 //
-// Measured: six chats of up to 32,013 positions, 4 heads of 256, 338 MB of keys
-// and values in 61 us (5.5 TB/s; 128-byte rows and longer read at 5.1 - 6.1 TB/s
-// here); 64 streams over e4m3 pages, 1.33 GB in 266 us (5.0 TB/s); one chat of 310
-// positions 11 us, the latency of its five dependent loads, two products and join.
+// Measured, a call with inputs that the caches do not hold: six chats of up to
+// 32,013 positions, 4 heads of 256, 338 MB of keys and values in 67 us (5.0 TB/s;
+// 128-byte rows and longer read at 5.1 - 6.1 TB/s here); 64 streams over e4m3 pages,
+// 1.33 GB in 270 us (4.9 TB/s); one chat of 310 positions 12 us, the latency of its
+// five dependent loads, two products and join.
 #include "lora_attn_core.h"
 
 namespace lora {

@@ -15,8 +15,8 @@
 // Measured: six prompts of up to 2,022 rows, 16 heads of 64, 28 us (50 us with 128
 // positions a block and rows through registers).  With the attention before it:
 // 4,000 rows and a suffix of 500 behind 8,500 positions, 16 heads of 256 over 4,
-// 428 us (567 us with one block for all rows of 64 positions); three prompts of up
-// to 2,176 rows, 5 heads of 128 over 1 under a window with sinks, 51 us (192 us).
+// 424 us (567 us with one block for all rows of 64 positions); three prompts of up
+// to 2,176 rows, 5 heads of 128 over 1 under a window with sinks, 52 us (192 us).
 #include "lora_attn_core.h"
 
 namespace lora {

@@ -10,7 +10,8 @@ namespace {
 // written once.  A block takes kAppendRows consecutive rows, looks their pages
 // up once, and streams their k and v in 16-byte pieces, kAppendDepth a thread at
 // a time (one at a time: 29 us).  16,002 rows of 4 heads of 256: 131 MB in 26.5 us,
-// 4.9 TB/s, as a large copy; 64 rows: 6.4 us, a launch and a load behind a load.
+// 4.9 TB/s, as a large copy; of 8 heads of 128 to e4m3 codes, 98 MB in 24 us, 4.1 TB/s (a
+// division an element, 8-byte stores); 64 rows: 6.7 us, a launch and a load behind a load.
 constexpr int kAppendRows = 4;
 constexpr int kAppendDepth = 4;   // pieces a thread has under way
 
@@ -96,7 +97,7 @@ constexpr int kSelWaves = kSelThreads / 64;
 // highest key, which no weight has.  The last key is found by radix selection: a
 // histogram of its top bits in LDS, the bin that holds the budget's end, then the
 // next bits among the keys of that bin.  One block takes one (sequence, head):
-// 20 us for 24 of up to 32,013 weights (67 us with five passes over memory), 24 us
+// 21 us for 24 of up to 32,013 weights (67 us with five passes over memory), 24 us
 // for 512 of up to 9,832.
 constexpr uint32_t kStays = 0xFFFFFFFFu;
 
@@ -285,7 +286,8 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(EvictArgs a) 
 }
 
 // Sequences of more positions than registers hold: every pass reads the weights again, eight key bits a
-// pass, and the kept positions leave in order.
+// pass, and the kept positions leave in order.  One such sequence takes its whole batch here: 85 us for 24
+// weights of up to 40,001, 247 us for 8 of 131,072.
 __global__ __launch_bounds__(kSelThreads) void evict_select_long_kernel(EvictArgs a) {
   __shared__ uint32_t hist[256];
   __shared__ uint32_t sel[2];
@@ -378,7 +380,7 @@ constexpr int kGatherRows = 64;
 
 // Copies kept rows to their new slots, and their weights; blockIdx.y is the head, z the sequence (their
 // product may pass 65,535, which a dimension of a grid is documented to hold).  Bound by bytes:
-// 101 MB of 512-byte rows in 17 us (5.8 TB/s), 786 MB of 128-byte rows in 160 us (4.9 TB/s).
+// 101 MB of 512-byte rows in 21 us (4.8 TB/s), 786 MB of 128-byte rows in 167 us (4.7 TB/s).
 __global__ __launch_bounds__(256) void evict_gather_kernel(EvictArgs a, int elem_bytes, uint32_t nan_word) {
   __shared__ int64_t src[kGatherRows], dst[kGatherRows];   // byte offsets; -1: no row, -2: source page invalid
   const int i = blockIdx.z, h = blockIdx.y;
