@@ -9,7 +9,9 @@
  * 1,552 tokens; section 7: several requests at once).  Three calls share one
  * cache and one table of sequences:
  *
- *   lora_kv_append   stores the batch's new keys and values in the pages
+ *   lora_kv_append   stores the batch's new keys and values in the pages;
+ *                    lora_kv_append_rope rotates keys by their positions on the
+ *                    way, and the batch's queries beside them
  *   lora_attn        the batch's query rows over the pages, causal, optionally
  *                    with a sliding window and first tokens that stay visible;
  *                    optionally accumulates the weight each position received
@@ -43,11 +45,23 @@
  *
  * Precision.  q, out and new rows are bf16 or fp16.  The cache holds the same
  * type, or e4m3 (OCP, largest value 448) with one fp32 scale per key-value head
- * for k and for v: value = code * scale.  Scores, the softmax's statistics,
+ * for k and for v: value = code * scale; or e2m1 in blocks (below).  Scores, the softmax's statistics,
  * sums over positions and accumulated weights are fp32; out is rounded once at
  * the store.  Before they meet v, decoded rows' weights are split into two
  * numbers of q's type, which hold twice its bits; prompts' weights are rounded
  * once, to q's type, or to fp16 over an E4M3 cache.
+ *
+ * Blocks of 4 bits.  An E2M1 cache holds the OCP microscaling format MXFP4: codes of
+ * 0, 0.5, 1, 1.5, 2, 3, 4 and 6 with a sign, two a byte, the lower dimension in the low
+ * four bits, and for each run of 32 of a head's dimensions one byte E, a power of two:
+ * value = code * 2^(E - 127), and NaN where E is 255.  That is 4.25 bits a value.  The
+ * exponents lie in a pool of their own that has the codes' order: a row's start at a
+ * sixteenth of the codes' byte offset, so the two pools are (pages, slots, heads,
+ * head_dim / 2) and (pages, slots, heads, head_dim / 32) bytes in the same order of
+ * dimensions.  Heads outside slots keep 16 slots of a head together, which is what a
+ * block reads (64 decoding streams, 8 heads of 128, the other way: a cache line holds two
+ * heads).  Values meet queries and weights in the queries' type, which holds them exactly
+ * but for fp16 past 65504 (infinite there) and below 2^-24 (rounded).
  *
  * Limits (LORA_EUNSUPPORTED beyond): head_dim 64, 128 or 256; page_size a
  * multiple of 16 up to 65536; n_seq <= LORA_MAX_SEGMENTS; kv_len <= 2^24;
@@ -77,16 +91,17 @@ extern "C" {
 typedef enum lora_kv_dtype {
   LORA_KV_BF16 = 0,
   LORA_KV_F16 = 1,
-  LORA_KV_E4M3 = 2        /* caches only */
+  LORA_KV_E4M3 = 2,       /* caches only */
+  LORA_KV_E2M1 = 4        /* caches only */
 } lora_kv_dtype;
 
 typedef struct lora_kv_cache {
   void* k;                /* device */
   void* v;                /* device, the same strides */
-  const float* k_scale;   /* device, n_kv_heads fp32: E4M3 only, else NULL */
-  const float* v_scale;
+  const void* k_scale;    /* device; E4M3: n_kv_heads fp32; E2M1: the blocks' exponents, a byte each; else NULL */
+  const void* v_scale;
   int64_t n_pages;        /* 1 .. 2^31 - 1 */
-  int64_t page_stride;    /* in elements, each at least head_dim */
+  int64_t page_stride;    /* in elements (E2M1: two a byte), each at least head_dim */
   int64_t token_stride;
   int64_t head_stride;
   int32_t page_size;      /* slots per page */
@@ -108,8 +123,14 @@ typedef struct lora_kv_batch {
  *
  *   k, v        device, (rows, n_kv_heads, head_dim) of `dtype`; row r, head h at
  *               r * row_stride + h * head_stride elements (views of a q|k|v projection's rows)
- *   dtype       LORA_KV_BF16 or LORA_KV_F16: the cache's type, or any when the cache is E4M3,
- *               which stores round-to-nearest-even(clamp(x / scale, -448, 448)), NaN as NaN
+ *   dtype       LORA_KV_BF16 or LORA_KV_F16: the cache's type, or any when the cache is E4M3 or E2M1
+ *
+ * E4M3 stores round-to-nearest-even(clamp(x / scale, -448, 448)), NaN as NaN.
+ *
+ * E2M1 gives a block the smallest power of two that leaves no value further than half a step from
+ * a code's: with a = max |x| of the block, E - 127 = floor(log2 a) - 2, one more where
+ * a > 7 * 2^(floor(log2 a) - 2), within -127 and 125 (bf16 rows) or 13 (fp16 rows); codes are x / 2^(E - 127) rounded to nearest,
+ * ties to even, values past 6 (infinities among them) held at 6.  A block with a NaN gets E 255.
  *
  * k and v must not overlap the cache (LORA_EINVAL).
  */
@@ -117,12 +138,57 @@ lora_status lora_kv_append(const lora_kv_cache* cache, const lora_kv_batch* batc
                            const void* k, const void* v, int64_t row_stride, int64_t head_stride,
                            lora_kv_dtype dtype, hipStream_t stream);
 
+/* Rotary positions.  Frequency j of dim / 2 turns the pair (x_j, x_{j + dim/2}), or (x_2j, x_{2j+1})
+ * where `interleaved` is set, of every head's first `dim` dimensions by the angle
+ *
+ *     f_j * positions[axis_j][row]
+ *
+ * and scales it by `factor`; dimensions from `dim` on stay as they are.  One axis is a text's position;
+ * several are those of images and video (time, height, width), each frequency with its own.
+ * Angles are exact: a frequency is held as a fraction of a turn in 64 bits, whose product with a
+ * position is reduced before anything is rounded, so the largest positions lose nothing. */
+typedef struct lora_rope {
+  const uint64_t* turns;      /* device, dim / 2: lora_rope_turns of the frequencies */
+  const uint8_t* axis;        /* HOST, dim / 2, each below n_axes; NULL: axis 0 */
+  const int32_t* positions;   /* device, n_axes runs of the batch's rows, any int32; NULL: a row's position in its
+                                 sequence (the slot its key is stored at) on every axis */
+  int64_t position_stride;    /* entries from run to run, at least the rows; 0: one run serves every axis */
+  int32_t n_axes;             /* 1 .. 4 */
+  int32_t dim;                /* rotated dimensions of a head: a multiple of 16, at most head_dim */
+  int32_t interleaved;
+  float factor;               /* finite; 1 unless a scaling of positions has one */
+} lora_rope;
+
+/* turns[j] = round(2^64 * f_j / (2 pi)) modulo 2^64 for n frequencies in radians a position; HOST arrays.
+ * LORA_EINVAL for one that is not finite. */
+lora_status lora_rope_turns(const double* freqs, int32_t n, uint64_t* turns);
+
+/*
+ * lora_kv_append_rope — lora_kv_append with the new keys rotated, and the batch's queries beside them.
+ *
+ *   rope        the rotation
+ *   q           device, (rows, n_heads, head_dim) of `dtype`, row r, head c at r * q_row_stride +
+ *               c * q_head_stride elements; NULL with n_heads 0: keys and values alone
+ *   n_heads     a multiple of the cache's n_kv_heads, or 0
+ *   q_out       device, (rows, n_heads, head_dim) contiguous, fully overwritten; must not overlap q, k, v,
+ *               the cache or the rotation's arrays (LORA_EINVAL)
+ *
+ * Rotation is fp32 and rounded once, to q_out's type or the cache's.  Values are stored as they are.
+ * A position that was evicted keeps the rotation it was appended with, so positions of later rows
+ * of its sequence are then given, since slots count kept positions only.
+ */
+lora_status lora_kv_append_rope(const lora_kv_cache* cache, const lora_kv_batch* batch,
+                                const void* k, const void* v, int64_t row_stride, int64_t head_stride,
+                                lora_kv_dtype dtype, const lora_rope* rope,
+                                const void* q, int64_t q_row_stride, int64_t q_head_stride, int32_t n_heads,
+                                void* q_out, hipStream_t stream);
+
 /*
  * lora_attn — attention of the batch's rows over the cache.
  *
  *   q           device, (rows, n_heads, head_dim) of `dtype`, row r, head c at
  *               r * q_row_stride + c * q_head_stride elements
- *   dtype       LORA_KV_BF16 or LORA_KV_F16; the cache's type unless that is E4M3
+ *   dtype       LORA_KV_BF16 or LORA_KV_F16; the cache's type unless that is E4M3 or E2M1
  *   n_heads     a multiple of the cache's n_kv_heads
  *   window      positions a row sees up to itself; negative: all
  *   sinks       first positions that stay visible outside the window

@@ -6,7 +6,7 @@ every layer's cache:
     cache = KVCache(k_pages, v_pages)                 # (n_pages, page_size, kv_heads, head_dim) each
     batch = KVBatch(q_starts, kv_len, page_table)     # host sequences and an int32 device table
     qkv = lora_proj(x, ..., slices=[...])             # (rows, (heads + 2 kv_heads) head_dim)
-    kv_append(cache, batch, k, v)                     # k, v: views of qkv, (rows, kv_heads, head_dim)
+    q = kv_append(cache, batch, k, v, rope, q=q)      # k, v, q: views of qkv, (rows, heads, head_dim); q comes rotated
     y = attn(cache, batch, q)                         # (rows, heads, head_dim)
 
 As in the rest of the package, these wrappers marshal arguments and every step
@@ -18,7 +18,7 @@ import ctypes
 
 from . import binding as _bd
 
-KV_DTYPES = {"bf16": 0, "f16": 1, "e4m3": 2}
+KV_DTYPES = {"bf16": 0, "f16": 1, "e4m3": 2, "e2m1": 4}
 
 
 def _i32(x):
@@ -46,35 +46,101 @@ def _strides3(name, t, dim):
 class KVCache:
     """Pages of keys and values: two (n_pages, page_size, kv_heads, head_dim) CUDA tensors of the same
     strides, the last dimension contiguous (any order of the others: permute a head-major pool).
-    bfloat16, float16, or float8_e4m3fn with ``k_scale`` and ``v_scale`` (kv_heads float32 each)."""
+    bfloat16, float16, or float8_e4m3fn with ``k_scale`` and ``v_scale`` (kv_heads float32 each).
+
+    A pool of uint8 or float4_e2m1fn_x2, (n_pages, page_size, kv_heads, head_dim / 2), is a cache in 4 bits:
+    two e2m1 codes a byte, and ``k_scale`` and ``v_scale`` are (n_pages, page_size, kv_heads, head_dim / 32)
+    exponents of the same order of dimensions, uint8 or float8_e8m0fnu.  Head-major pools read fastest."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         import torch
-        kinds = {torch.bfloat16: "bf16", torch.float16: "f16", torch.float8_e4m3fn: "e4m3"}
+        kinds = {torch.bfloat16: "bf16", torch.float16: "f16", torch.float8_e4m3fn: "e4m3", torch.uint8: "e2m1",
+                 torch.float4_e2m1fn_x2: "e2m1"}
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in kinds:
             raise ValueError("k and v must be (n_pages, page_size, kv_heads, head_dim) of one type: bfloat16, "
-                             "float16 or float8_e4m3fn")
+                             "float16, float8_e4m3fn, or uint8 of two 4-bit codes")
         _bd._check_operands(k.device, {"k": k, "v": v, "k_scale": k_scale, "v_scale": v_scale})
         self.dtype = kinds[k.dtype]
-        if (self.dtype == "e4m3") != (k_scale is not None) or (k_scale is None) != (v_scale is None):
-            raise ValueError("k_scale and v_scale go with a float8_e4m3fn cache")
-        for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
-            if s is not None and (s.dtype != torch.float32 or tuple(s.shape) != (k.shape[2],) or not s.is_contiguous()):
-                raise ValueError(f"{name} must be {k.shape[2]} contiguous float32 values")
+        if (self.dtype in ("e4m3", "e2m1")) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+            raise ValueError("k_scale and v_scale go with a float8_e4m3fn cache or one of 4-bit codes")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.device = k.device
         self.n_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
-        stride = lambda t: [t.stride(i) if t.shape[i] > 1 else max(self.head_dim, 16) for i in range(3)]
-        if stride(k) != stride(v) or k.stride(3) != 1 or v.stride(3) != 1:
+        per = 2 if self.dtype == "e2m1" else 1            # elements in one of the tensor's
+        self.head_dim *= per
+        stride = lambda t, one: [t.stride(i) if t.shape[i] > 1 else one for i in range(3)]
+        strides = stride(k, max(self.head_dim // per, 16))
+        if strides != stride(v, max(self.head_dim // per, 16)) or k.stride(3) != 1 or v.stride(3) != 1:
             raise ValueError("k and v must have the same strides and a contiguous last dimension")
-        page, token, head = stride(k)
+        for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if self.dtype == "e4m3" and (s.dtype != torch.float32 or tuple(s.shape) != (self.kv_heads,) or
+                                         not s.is_contiguous()):
+                raise ValueError(f"{name} must be {self.kv_heads} contiguous float32 values")
+            if self.dtype == "e2m1" and (
+                    s.dtype not in (torch.uint8, torch.float8_e8m0fnu) or s.dim() != 4 or
+                    s.shape[:3] != k.shape[:3] or s.shape[3] * 32 != self.head_dim or s.stride(3) != 1 or
+                    any(s.shape[i] > 1 and s.stride(i) * 16 != strides[i] for i in range(3))):
+                raise ValueError(f"{name} must be (n_pages, page_size, kv_heads, head_dim / 32) exponents (uint8 or "
+                                 "float8_e8m0fnu) of the codes' order, every stride a sixteenth of theirs")
+        page, token, head = (x * per for x in strides)
         self._c = _bd.KVCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if k_scale is not None else None,
                                     v_scale.data_ptr() if v_scale is not None else None, self.n_pages, page, token,
                                     head, self.page_size, self.kv_heads, self.head_dim, KV_DTYPES[self.dtype])
         self._ref = ctypes.byref(self._c)
         self._index = k.get_device()
         # the types of new rows and queries that go with the cache, and their codes
-        self._row_codes = {torch.bfloat16: 0, torch.float16: 1} if self.dtype == "e4m3" else {k.dtype: KV_DTYPES[self.dtype]}
+        self._row_codes = {torch.bfloat16: 0, torch.float16: 1} if k_scale is not None else {k.dtype: KV_DTYPES[self.dtype]}
+
+
+class Rope:
+    """A rotation of the first ``dim`` dimensions of a head by its row's position.
+
+    Frequency j of dim / 2 is ``base ** (-2 j / dim)`` radians a position, or ``freqs[j]`` where positions are
+    scaled; it turns the dimensions j and j + dim / 2, or 2 j and 2 j + 1 with ``interleaved``.  ``axis`` names
+    each frequency's axis of positions (0 .. 3) where those are of several (time, height, width):
+
+        Rope(128, axis=[0] * 16 + [1] * 24 + [2] * 24)      # in runs
+        Rope(128, axis=[j % 3 for j in range(64)])          # in turns
+
+    ``factor`` multiplies what is rotated.  One Rope serves every layer of a GPU."""
+
+    def __init__(self, dim, base=10000.0, freqs=None, axis=None, interleaved=False, factor=1.0, device=None):
+        import torch
+        self.dim, self.factor, self.interleaved = int(dim), float(factor), bool(interleaved)
+        if self.dim < 2 or self.dim % 2:
+            raise ValueError("dim must be an even number of dimensions")
+        half = self.dim // 2
+        freqs = [float(base) ** (-2.0 * j / self.dim) for j in range(half)] if freqs is None else [float(f) for f in freqs]
+        axis = [0] * half if axis is None else [int(a) for a in axis]
+        if len(freqs) != half or len(axis) != half:
+            raise ValueError(f"freqs and axis hold {half} entries each, one for a pair of dimensions")
+        if min(axis) < 0 or max(axis) > 3:
+            raise ValueError("axis must be 0 .. 3")
+        self.freqs, self.axis, self.axes = freqs, axis, max(axis) + 1
+        turns = (ctypes.c_uint64 * half)()
+        status = _bd.load().lora_rope_turns((ctypes.c_double * half)(*freqs), half, turns)
+        if status != _bd.LORA_OK:
+            raise ValueError("freqs must be finite")
+        device = torch.device("cuda" if device is None else device)
+        self._turns = torch.tensor([x - (1 << 64) if x >> 63 else x for x in turns], dtype=torch.int64, device=device)
+        self._index = self._turns.get_device()
+        self._axis = (ctypes.c_uint8 * half)(*axis)
+
+    def _struct(self, positions, rows):
+        """The library's rotation, and the tensor it points to kept beside it."""
+        import torch
+        at, stride, axes = None, 0, self.axes
+        if positions is not None:
+            if positions.dtype != torch.int32 or positions.get_device() != self._index or positions.dim() not in (1, 2):
+                raise ValueError("positions must be an int32 CUDA tensor (rows,) or (axes, rows) on the Rope's GPU")
+            if positions.shape[-1] != rows or (rows > 1 and positions.stride(-1) != 1):
+                raise ValueError(f"positions must hold the batch's {rows} rows, contiguous")
+            given = positions.shape[0] if positions.dim() == 2 else 1
+            if given < axes:
+                raise ValueError(f"positions hold {given} axes, the Rope takes {axes}")
+            at, stride = positions.data_ptr(), positions.stride(0) if positions.dim() == 2 and given > 1 else rows
+        return _bd.RopeStruct(self._turns.data_ptr(), ctypes.cast(self._axis, ctypes.c_void_p), at, stride, axes,
+                              self.dim, int(self.interleaved), self.factor)
 
 
 class KVBatch:
@@ -174,17 +240,44 @@ def _call(cache, entry, *args):
         raise _bd.LoraError(status, _bd.status_string(status))
 
 
-def kv_append(cache, batch, k, v, stream=None):
+def kv_append(cache, batch, k, v, rope=None, positions=None, q=None, q_out=None, stream=None):
     """Store the batch's new rows k, v (rows, kv_heads, head_dim; equal strides) at the last positions of
-    their sequences, rounded to e4m3 codes of x / scale when the cache holds those."""
+    their sequences, as codes where the cache holds those.
+
+    With a ``rope`` keys are rotated on the way, and the batch's queries ``q`` (rows, heads, head_dim; rows and
+    heads may be strided), where they are given, into ``q_out``, which is returned.  ``positions``: int32
+    (rows,) or (axes, rows); without them a row's position in its sequence, on every axis."""
     _check_batch(cache, batch)
     code = _row_code(cache, batch, "k", k)
     strides = _strides3("k", k, cache.head_dim)
     if code != _row_code(cache, batch, "v", v) or k.shape != v.shape or k.shape[1] != cache.kv_heads or \
             strides != _strides3("v", v, cache.head_dim):
         raise ValueError("k and v must be (rows, kv_heads, head_dim) of one type and the same strides")
-    _call(cache, _bd.load().lora_kv_append, cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), strides[0], strides[1],
-          code, _handle(stream, cache))
+    if rope is None:
+        if positions is not None or q is not None or q_out is not None:
+            raise ValueError("positions, q and q_out go with a rope")
+        _call(cache, _bd.load().lora_kv_append, cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), strides[0],
+              strides[1], code, _handle(stream, cache))
+        return None
+    if rope._index != cache._index:
+        raise ValueError(f"the Rope is on GPU {rope._index}, the cache on {cache.device}")
+    turn = rope._struct(positions, batch.rows)
+    s = _handle(stream, cache)
+    heads, q_strides, q_at, out_at = 0, (0, 0), None, None
+    if q is not None:
+        if code != _row_code(cache, batch, "q", q):
+            raise ValueError("q must be of the type of k and v")
+        q_strides, heads, q_at = _strides3("q", q, cache.head_dim), q.shape[1], q.data_ptr()
+        if q_out is None:
+            q_out = _empty(q.shape, q.dtype, cache.device, stream)
+        elif q_out.dtype != q.dtype or q_out.device != cache.device or not q_out.is_contiguous() or q_out.shape != q.shape:
+            raise ValueError("q_out must be a contiguous tensor like q")
+        out_at = q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out goes with q")
+    _call(cache, _bd.load().lora_kv_append_rope, cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), strides[0],
+          strides[1], code, ctypes.byref(turn), q_at, q_strides[0], q_strides[1], heads, out_at, s)
+    return q_out
 
 
 def attn_workspace_bytes(cache, batch, heads, window=-1, sinks=0, mass=False):

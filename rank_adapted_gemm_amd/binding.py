@@ -27,7 +27,8 @@ EXPORTS = ("lora_proj", "lora_proj_ex", "lora_proj_multi", "lora_proj_sliced", "
            "lora_proj_path", "lora_proj_tile_rows", "lora_status_string", "lora_extract", "lora_extract_workspace_bytes",
            "lora_probe_mfma_bf16", "lora_probe_read", "lora_workspace_status", "lora_debug_handover_fault",
            "lora_decode_plan_describe", "lora_proj_noalloc", "lora_proj_ranked", "lora_kv_append", "lora_attn",
-           "lora_attn_workspace_bytes", "lora_attn_plan_describe", "lora_kv_evict")
+           "lora_attn_workspace_bytes", "lora_attn_plan_describe", "lora_kv_evict", "lora_rope_turns",
+           "lora_kv_append_rope")
 NOALLOC_SCRATCH_BYTES = 64 << 20   # the device array lora_proj_noalloc uses instead of a workspace
 PLAN_FIELDS = ("MT", "nst", "nrs", "ntA", "ntW", "n_used", "GA", "GW", "smaxW", "off_cnt", "off_pa", "pa_bytes",
                "off_pw", "pw_bytes", "off_th", "t_bytes", "off_tl", "total")
@@ -48,6 +49,13 @@ class KVBatchStruct(ctypes.Structure):
     """lora_kv_batch (lora_attn.h)."""
     _fields_ = [("q_starts", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
                 ("table_stride", ctypes.c_int64), ("n_seq", ctypes.c_int32)]
+
+
+class RopeStruct(ctypes.Structure):
+    """lora_rope (lora_attn.h)."""
+    _fields_ = [("turns", ctypes.c_void_p), ("axis", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("position_stride", ctypes.c_int64), ("n_axes", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("factor", ctypes.c_float)]
 
 
 class LoraError(RuntimeError):
@@ -117,6 +125,10 @@ def load():
     lib.lora_decode_plan_describe.restype = i32
     lib.lora_kv_append.argtypes = [vp, vp, vp, vp, i64, i64, ctypes.c_int, vp]
     lib.lora_kv_append.restype = ctypes.c_int
+    lib.lora_rope_turns.argtypes = [vp, i32, vp]
+    lib.lora_rope_turns.restype = ctypes.c_int
+    lib.lora_kv_append_rope.argtypes = [vp, vp, vp, vp, i64, i64, ctypes.c_int, vp, vp, i64, i64, i32, vp, vp]
+    lib.lora_kv_append_rope.restype = ctypes.c_int
     lib.lora_attn.argtypes = [vp, vp, vp, i64, i64, i32, ctypes.c_int, ctypes.c_float, i32, i32, vp, vp, vp, i64,
                               vp, sz, vp]
     lib.lora_attn.restype = ctypes.c_int

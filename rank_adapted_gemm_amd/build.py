@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "liblora_proj.so"
 SOURCES = ["lora_api.cpp", "lora_bf16.hip", "lora_decode.hip", "lora_f32.hip", "lora_q4.hip", "lora_extract.hip",
            "lora_probe.hip", "lora_kv_api.cpp", "lora_kv.hip", "lora_attn.hip",
-           "lora_attn_decode.hip", "lora_attn_mass.hip"]
+           "lora_attn_decode.hip", "lora_attn_decode4.hip", "lora_attn_mass.hip", "lora_kv_rope.hip"]
 ARCH = "gfx950"
 
 

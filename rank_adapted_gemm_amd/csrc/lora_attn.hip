@@ -86,21 +86,27 @@ struct WeightType<__bf16, true> {
 };
 
 // 64-wide heads leave registers for two blocks a CU.
-template <typename T, bool F8, int DIM>
+//
+// F4: e2m1 pages.  A wave brings its 16 positions' codes to a stage of its own in LDS two steps ahead, and a step
+// ahead makes T of them in the tile, so that products, borders and hidden values are those of 16-bit pages and each
+// code is converted once a block.
+template <typename T, bool F8, int DIM, bool F4>
 __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(AttnArgs a, AttnPart part) {
   using R = Row<F8, DIM>;
   using x8 = typename Vec<T>::x8;
   using W = typename WeightType<T, F8>::type;
   using w8 = typename Vec<W>::x8;
   constexpr int BM = kWaves * 32, TILE = kBN * R::kBytes, KS = DIM / 16, DB = DIM / 32;
+  // e2m1: blocks (16 bytes of codes) of a row, wave-wide loads of 16 rows, and how many steps ahead those are
+  constexpr int BLK = DIM / 32, PIECES = (16 * BLK + 63) / 64, STAGE = F4 ? kWaves * PIECES * 1024 : 0, LOOK = F4 ? 2 : 1;
   constexpr int KR = F8 ? KS / 2 : KS;   // LDS reads of 32 positions' keys
   // Fragments read ahead of the products.  256-wide heads: three, four take registers that the addresses
   // need (a 4,096 window over 16,002 rows: 854 against 868 us); narrower ones: four (8,000 rows of 32 heads of
   // 128 over e4m3 pages: 523 against 526 us with three, though 495 against 489 over bf16 ones).
   constexpr int kAhead = DIM == 256 ? 3 : 4;
   static_assert(BM == kPromptRows, "one tile height for the host's plan");
-  __shared__ __attribute__((aligned(1024))) char lds[4 * TILE];   // keys, keys, values, values
-  __shared__ __attribute__((aligned(16))) int32_t bad[2][4];      // invalid 16-slot groups of a step
+  __shared__ __attribute__((aligned(1024))) char lds[4 * TILE + STAGE];   // keys, keys, values, values; codes
+  __shared__ __attribute__((aligned(16))) int32_t bad[2 * LOOK][4];       // invalid 16-slot groups of a step
   __shared__ int32_t hit[2];                                      // steps (from 1) whose values held an infinity or NaN
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -149,7 +155,7 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
   const uint32_t row_off = uint32_t(lrow) * uint32_t(a.c.token_stride);
   const uint32_t chunk_off = uint32_t((lslot ^ (values ? V::swizzle(lrow) : R::key_swizzle(lrow))) << 4);
   char* const pool = (values ? a.c.v : a.c.k) + int64_t(item.head) * a.c.head_stride;
-  const uint32_t group_bytes = uint32_t(15 * a.c.token_stride + R::kBytes);
+  const uint32_t group_bytes = uint32_t(15 * a.c.token_stride + (F4 ? DIM / 2 : R::kBytes));
   // where the group lies in the pool in steps (it & ~63) + lane; high word -1: not needed, -2: invalid
   int32_t place_lo = 0, place_hi = -1;
   bool somebad = false;   // some step of these 64 has an invalid group
@@ -171,17 +177,57 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
         invalid = page == -1;
       }
     }
-    somebad = __builtin_amdgcn_readfirstlane(__syncthreads_or(invalid)) != 0;
+    // with steps of two batches under way, once is for good
+    somebad = __builtin_amdgcn_readfirstlane(__syncthreads_or(invalid)) != 0 || (F4 && somebad);
   };
-  i32x4 rs;   // the next step's group
+  i32x4 rs;       // the next step's group
+  i32x4 rs_exp;   // e2m1: its exponents
   auto aim = [&](int it) {
     const int hi = __builtin_amdgcn_readlane(place_hi, it & 63);
     const uint32_t lo = uint32_t(__builtin_amdgcn_readlane(place_lo, it & 63));
     const bool there = it < nu && hi >= 0;
-    rs = make_rsrc_words(pool + (there ? int64_t(hi) << 32 | lo : 0), there ? group_bytes : 0u);
-    if (somebad && !values && lane == 0) bad[it & 1][grp] = hi == -2;
+    const int64_t at = there ? int64_t(hi) << 32 | lo : 0;
+    rs = make_rsrc_words(pool + at, there ? group_bytes : 0u);
+    if constexpr (F4)
+      rs_exp = make_rsrc_words((values ? a.c.v_exp : a.c.k_exp) + ((int64_t(item.head) * a.c.head_stride + at) >> 4),
+                               there ? group_bytes >> 4 : 0u);
+    if (somebad && !values && lane == 0) bad[it & (2 * LOOK - 1)][grp] = hi == -2;
+  };
+  // e2m1: piece x of the group is 64 / BLK rows, a block a lane
+  const uint32_t stage = lds0 + 4 * TILE + wave * (PIECES * 1024);
+  const int prow = lane / BLK, pblk = lane % BLK;
+  const uint32_t code_off = uint32_t(prow) * uint32_t(a.c.token_stride) + uint32_t(pblk) * 16;
+  const uint32_t exp_off = uint32_t(prow) * (uint32_t(a.c.token_stride) >> 4) + uint32_t(pblk);
+  uint32_t exps[PIECES];
+  auto fetch = [&] {   // what aim() aimed at
+#pragma unroll
+    for (int x = 0; x < PIECES; ++x) {
+      const uint32_t rows = uint32_t(x * (64 / BLK)) * uint32_t(a.c.token_stride);
+      const bool there = 16 * BLK >= 64 || lane < 16 * BLK;   // 64-wide heads: half of a piece
+      dma16(rs, there ? code_off + rows : kDmaMaskedOffset, stage + x * 1024);
+      exps[x] = __builtin_amdgcn_raw_buffer_load_b8(rsrc_of_words(rs_exp), there ? exp_off + (rows >> 4) : 0xFFFFFFFFu, 0, 0);
+    }
+  };
+  auto convert = [&](int it) {   // the fetched step's codes, to its tile
+    typedef __attribute__((address_space(3))) u32x4* p16;
+    const uint32_t tile = lds0 + (values ? 2 * TILE : 0) + (it & 1) * TILE;
+#pragma unroll
+    for (int x = 0; x < PIECES; ++x) {
+      const int r = x * (64 / BLK) + prow;
+      const u32x4 w = *p16(uintptr_t(stage + x * 1024 + lane * 16));
+      const float s = scale_of(exps[x]);
+      const uint32_t row = tile + uint32_t(grp * 16 + r) * R::kBytes;
+      const uint32_t sw = uint32_t(pblk * 4) ^ uint32_t(values ? V::swizzle(r) : R::key_swizzle(r));
+      if (16 * BLK >= 64 || lane < 16 * BLK) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *p16(uintptr_t(row + ((sw ^ uint32_t(k)) << 4))) = __builtin_bit_cast(u32x4, from_e2m1<T>(w[k], s));
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");   // the stage may be filled again
   };
   auto load = [&](int it, int x) {   // one of the group's R::kLoads
+    if constexpr (F4) return;
     const int r = x * R::kRowsPerLoad;
     const uint32_t sw = uint32_t((values ? V::swizzle(r) : R::key_swizzle(r)) << 4);
     dma16(rs, row_off + uint32_t(r) * uint32_t(a.c.token_stride) + (chunk_off ^ sw),
@@ -289,8 +335,16 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
   };
 
   if (tid < 2) hit[tid] = 0;
+  if (F4 && tid < 8 * LOOK) bad[tid >> 2][tid & 3] = 0;
   load_pages(0);
   aim(0);
+  if constexpr (F4) {
+    fetch();
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+    convert(0);
+    aim(1);
+    fetch();
+  }
 #pragma unroll
   for (int x = 0; x < R::kLoads; ++x) load(0, x);
   for (int it = 0; it < nu;) {
@@ -300,8 +354,8 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
       const uint32_t kt = lds0 + (it & 1) * TILE, vt = kt + 2 * TILE;
       constexpr int EARLY = (R::kLoads + 1) / 2, LATE = R::kLoads - EARLY;   // with the scores, with the outputs
       meet();
-      if (((it + 1) & 63) == 0) load_pages(it + 1);
-      aim(it + 1);
+      if (((it + LOOK) & 63) == 0) load_pages(it + LOOK);
+      aim(it + LOOK);
       // Waves w and w + 4 share a SIMD and leave the barrier together.  At 64-wide heads, where a step is
       // short and mostly exponentials, 128 cycles' delay of one lets its products run beside the other's
       // exponentials (300 rows of 8 heads: 11.2 -> 11.0 us, 8,000 of 16 the same; wider heads gain nothing).
@@ -312,6 +366,10 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
 #pragma unroll
         for (int x = EARLY * n / of; x < EARLY * (n + 1) / of; ++x) load(it + 1, x);
       });
+      if constexpr (F4) {
+        convert(it + 1);
+        fetch();
+      }
       weights(st, w);
       outputs(vt, w, [&](int n, int of) {
 #pragma unroll
@@ -327,11 +385,15 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
     const int unit0 = units.unit(u0 + it) * kBN, buf = it & 1;
     uint32_t anybad = 0;
     if (somebad) {
-      const u32x4 bw = *reinterpret_cast<const u32x4*>(bad[buf]);
+      const u32x4 bw = *reinterpret_cast<const u32x4*>(bad[it & (2 * LOOK - 1)]);
       anybad = __builtin_amdgcn_readfirstlane(bw[0] | bw[1] << 1 | bw[2] << 2 | bw[3] << 3);
     }
-    if (((it + 1) & 63) == 0) load_pages(it + 1);
-    aim(it + 1);
+    if (((it + LOOK) & 63) == 0) load_pages(it + LOOK);
+    aim(it + LOOK);
+    if constexpr (F4) {
+      convert(it + 1);
+      fetch();
+    }
 #pragma unroll
     for (int x = 0; x < R::kLoads; ++x) load(it + 1, x);
     // A position that a row does not see may hold anything there, and its weight 0 must not meet an
@@ -378,7 +440,7 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
 
   if (again) {
     for (int m = mw; m < min(m1, mw + 32); ++m)
-      slow_row<T, F8, DIM>(a, sq, pages, units, u0, nu, kBN, t0, item.head, m,
+      slow_row<T, F8, DIM, F4>(a, sq, pages, units, u0, nu, kBN, t0, item.head, m,
                            sq.nsplit > 1 ? int64_t(blockIdx.x) * BM + (m - m0) : -1,
                            sq.nsplit > 1 ? int64_t(blockIdx.x) * BM + (m - m0) : -1);
     return;
@@ -422,12 +484,12 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
   if (a.lse && hh == 0 && m < m1) a.lse[row] = total == 0 ? -INFINITY : top + __builtin_log2f(total);
 }
 
-template <typename T, bool F8>
+template <typename T, bool F8, bool F4 = false>
 hipError_t run_prompt(const AttnArgs& a, const AttnPart& p, hipStream_t stream) {
   const dim3 grid(p.items), block(512);
-  if (a.c.dim == 256) hipLaunchKernelGGL((prompt_kernel<T, F8, 256>), grid, block, 0, stream, a, p);
-  else if (a.c.dim == 128) hipLaunchKernelGGL((prompt_kernel<T, F8, 128>), grid, block, 0, stream, a, p);
-  else hipLaunchKernelGGL((prompt_kernel<T, F8, 64>), grid, block, 0, stream, a, p);
+  if (a.c.dim == 256) hipLaunchKernelGGL((prompt_kernel<T, F8, 256, F4>), grid, block, 0, stream, a, p);
+  else if (a.c.dim == 128) hipLaunchKernelGGL((prompt_kernel<T, F8, 128, F4>), grid, block, 0, stream, a, p);
+  else hipLaunchKernelGGL((prompt_kernel<T, F8, 64, F4>), grid, block, 0, stream, a, p);
   return hipGetLastError();
 }
 
@@ -435,6 +497,9 @@ hipError_t run_prompt(const AttnArgs& a, const AttnPart& p, hipStream_t stream) 
 
 hipError_t launch_attn_prompt(const AttnArgs& a, const AttnPart& p, int dtype, int cache_dtype, hipStream_t stream) {
   const bool f8 = cache_dtype == LORA_KV_E4M3;
+  if (cache_dtype == LORA_KV_E2M1)
+    return dtype == LORA_KV_BF16 ? run_prompt<__bf16, false, true>(a, p, stream)
+                                 : run_prompt<_Float16, false, true>(a, p, stream);
   if (dtype == LORA_KV_BF16) return f8 ? run_prompt<__bf16, true>(a, p, stream) : run_prompt<__bf16, false>(a, p, stream);
   return f8 ? run_prompt<_Float16, true>(a, p, stream) : run_prompt<_Float16, false>(a, p, stream);
 }

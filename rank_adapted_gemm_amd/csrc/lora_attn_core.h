@@ -76,6 +76,32 @@ __device__ __forceinline__ typename Vec<T>::x8 from_e4m3(uint32_t lo, uint32_t h
   return typename Vec<T>::x8{r[0][0], r[0][1], r[1][0], r[1][1], r[2][0], r[2][1], r[3][0], r[3][1]};
 }
 
+// Scale of a block whose exponent byte is e: 2^(e - 127).  The conversions below read its exponent bits alone, 0 as
+// 2^-127 and 255 as NaN.
+__device__ __forceinline__ float scale_of(uint32_t e) { return __builtin_bit_cast(float, e << 23); }
+
+// Eight e2m1 codes times their block's scale as T, rounded to it: exact in bf16, and in fp16 from 2^-24 to 65504.
+template <typename T>
+__device__ __forceinline__ typename Vec<T>::x8 from_e2m1(uint32_t codes, float scale) {
+  typename Vec<T>::x2 r[4];
+  if constexpr (__is_same(T, __bf16)) {
+    r[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0);
+    r[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1);
+    r[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2);
+    r[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3);
+  } else {
+    r[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 0);
+    r[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 1);
+    r[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 2);
+    r[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 3);
+  }
+  return typename Vec<T>::x8{r[0][0], r[0][1], r[1][0], r[1][1], r[2][0], r[2][1], r[3][0], r[3][1]};
+}
+
+// The first exponent byte under which a code may be infinite (or NaN) in T.
+template <typename T>
+constexpr uint32_t kFirstInfinite = __is_same(T, __bf16) ? 127 + 126 : 127 + 14;
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
   const f32x2 f = {a, b};
@@ -202,6 +228,14 @@ __device__ __forceinline__ int seq_of_item(const AttnPart& p, int b) {
   return __builtin_amdgcn_readfirstlane(s);
 }
 
+// Eight e2m1 values in fp32, from byte `off` of a pool.
+template <typename T>
+__device__ __forceinline__ void load8_e2m1(const char* pool, const uint8_t* exp, int64_t off, float (&f)[8]) {
+  const auto x = from_e2m1<T>(*reinterpret_cast<const uint32_t*>(pool + off), scale_of(exp[off >> 4]));
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = float(x[e]);
+}
+
 // Eight cached values in fp32 (e4m3: codes, without their scale).
 template <typename T, bool F8>
 __device__ __forceinline__ void load8(const char* p, float (&f)[8]) {
@@ -220,7 +254,7 @@ __device__ __forceinline__ void load8(const char* p, float (&f)[8]) {
 // score a lane, then a column (or few) a lane.  It only adds what the row sees, whatever the cache
 // holds elsewhere.  Writes the row's output, or its partial sums to `slot` where that is not negative,
 // and its maximum and sum to `ml_slot` or, there negative, their logarithm to lse.
-template <typename T, bool F8, int DIM>
+template <typename T, bool F8, int DIM, bool F4 = false>
 __device__ void slow_row(const AttnArgs& a, const AttnSeq& sq, const Pages& pages, const Units& units, int u0, int nu,
                          int unit_len, int t0, int head, int m, int64_t slot, int64_t ml_slot) {
   constexpr int EB = F8 ? 1 : 2, PER = DIM / 64;
@@ -247,7 +281,8 @@ __device__ void slow_row(const AttnArgs& a, const AttnSeq& sq, const Pages& page
         s = 0;
         for (int d = 0; d < DIM; d += 8) {
           float k[8], x[8];
-          load8<T, F8>(a.c.k + off + d * EB, k);
+          if constexpr (F4) load8_e2m1<T>(a.c.k, a.c.k_exp, off + d / 2, k);
+          else load8<T, F8>(a.c.k + off + d * EB, k);
           load8<T, false>(q + d * 2, x);
 #pragma unroll
           for (int e = 0; e < 8; ++e) s += k[e] * x[e];
@@ -269,6 +304,12 @@ __device__ void slow_row(const AttnArgs& a, const AttnSeq& sq, const Pages& page
       const float wl = __shfl(w, l);
       if (o < 0) continue;
       for (int e = 0; e < PER; ++e) {
+        if constexpr (F4) {
+          const int64_t at = o + (e * 64 + lane) / 2;
+          const uint32_t code = uint32_t(*reinterpret_cast<const uint8_t*>(a.c.v + at)) >> (lane & 1) * 4;
+          acc[e] += wl * float(from_e2m1<T>(code, scale_of(a.c.v_exp[at >> 4]))[0]);
+          continue;
+        }
         const char* v = a.c.v + o + (e * 64 + lane) * EB;
         acc[e] += wl * (F8 ? float(from_e4m3<T>(*reinterpret_cast<const uint8_t*>(v), 0)[0])
                            : float(*reinterpret_cast<const T*>(v)));

@@ -30,7 +30,7 @@ __device__ __forceinline__ void dma16_from(const char* p, uint32_t lds_addr) {
                "s"(__builtin_amdgcn_readfirstlane(lds_addr)) : "memory");
 }
 
-template <typename T, bool F8, int DIM>
+template <typename T, bool F8, int DIM, bool F4>
 __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_mass_kernel(AttnArgs a, AttnPart part) {
   using Q = Row<false, DIM>;   // rows of q are 16 bits wide whatever the cache holds
   using x8 = typename Vec<T>::x8;
@@ -73,7 +73,10 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_mass_ke
       const char* src = a.c.k + off + (x * 16 + hh * 8) * (F8 ? 1 : 2);
       u32x4 v = {0, 0, 0, 0};
       if (page >= 0) {
-        if constexpr (F8) {
+        if constexpr (F4) {
+          const int64_t at = off + x * 8 + hh * 4;
+          v = __builtin_bit_cast(u32x4, from_e2m1<T>(*reinterpret_cast<const uint32_t*>(a.c.k + at), scale_of(a.c.k_exp[at >> 4])));
+        } else if constexpr (F8) {
           const u32x2 w = *reinterpret_cast<const u32x2*>(src);
           v = __builtin_bit_cast(u32x4, from_e4m3<T>(w[0], w[1]));
         } else {
@@ -234,12 +237,12 @@ __global__ __launch_bounds__(256) void mass_join_kernel(AttnArgs a, AttnPart par
   a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.0f) + sum;
 }
 
-template <typename T, bool F8>
+template <typename T, bool F8, bool F4 = false>
 void run_mass(const AttnArgs& a, const AttnPart& p, hipStream_t stream) {
   const dim3 grid(p.items), block(256);
-  if (a.c.dim == 256) hipLaunchKernelGGL((prompt_mass_kernel<T, F8, 256>), grid, block, 0, stream, a, p);
-  else if (a.c.dim == 128) hipLaunchKernelGGL((prompt_mass_kernel<T, F8, 128>), grid, block, 0, stream, a, p);
-  else hipLaunchKernelGGL((prompt_mass_kernel<T, F8, 64>), grid, block, 0, stream, a, p);
+  if (a.c.dim == 256) hipLaunchKernelGGL((prompt_mass_kernel<T, F8, 256, F4>), grid, block, 0, stream, a, p);
+  else if (a.c.dim == 128) hipLaunchKernelGGL((prompt_mass_kernel<T, F8, 128, F4>), grid, block, 0, stream, a, p);
+  else hipLaunchKernelGGL((prompt_mass_kernel<T, F8, 64, F4>), grid, block, 0, stream, a, p);
 }
 
 }  // namespace
@@ -247,7 +250,10 @@ void run_mass(const AttnArgs& a, const AttnPart& p, hipStream_t stream) {
 hipError_t launch_attn_mass_prompt(const AttnArgs& a, const AttnPart& p, int dtype, int cache_dtype,
                                    hipStream_t stream) {
   const bool f8 = cache_dtype == LORA_KV_E4M3;
-  if (dtype == LORA_KV_BF16) {
+  if (cache_dtype == LORA_KV_E2M1) {
+    if (dtype == LORA_KV_BF16) run_mass<__bf16, false, true>(a, p, stream);
+    else run_mass<_Float16, false, true>(a, p, stream);
+  } else if (dtype == LORA_KV_BF16) {
     if (f8) run_mass<__bf16, true>(a, p, stream);
     else run_mass<__bf16, false>(a, p, stream);
   } else {

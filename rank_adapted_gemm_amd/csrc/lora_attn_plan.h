@@ -223,7 +223,7 @@ inline void attn_mass_part(AttnPart& p, const KvView& c, int group, int window, 
 }
 
 inline void attn_plan(AttnPlan& o, const KvView& c, const KvSeqs& s, int n_heads, int window, int sinks, bool mass,
-                      int elem_bytes) {
+                      int cache_dtype) {
   AttnWork dec[LORA_MAX_SEGMENTS], pro[LORA_MAX_SEGMENTS];
   int nd = 0, np = 0;
   const int group = n_heads / c.kv_heads;
@@ -263,8 +263,9 @@ inline void attn_plan(AttnPlan& o, const KvView& c, const KvSeqs& s, int n_heads
   std::sort(pro, pro + np, longer);
   // In units of 32 positions' keys and values of a head: a block's start costs what a CU streams meanwhile,
   // less where a second block streams beside it, and leaving sums their bytes twice.
-  const double unit_bytes = double(c.dim) * elem_bytes * 2 * (1 << kDecodeUnitShift);
-  const int dblocks = decode_blocks(c.dim, elem_bytes, o.decode_tile);
+  const double unit_bytes = double(kv_row_bytes(c.dim, cache_dtype)) * 2 * (1 << kDecodeUnitShift);
+  const int dblocks = cache_dtype == LORA_KV_E2M1 ? decode4_blocks(c.dim, o.decode_tile)
+                                                  : decode_blocks(c.dim, cache_dtype == LORA_KV_E4M3 ? 1 : 2, o.decode_tile);
   const int dchunk = attn_chunk(dec, nd, c.kv_heads, dblocks * kAttnCUs, (dblocks == 2 ? 32768 : 98304) / unit_bytes,
                                 o.decode_rows * c.dim * 8 / unit_bytes, 98304 / unit_bytes, 2, 0);
   attn_fill(o.decode, dec, nd, dchunk, s, c.kv_heads, o.decode_tile, group);

@@ -10,8 +10,10 @@ namespace lora {
 struct KvView {
   char* k;
   char* v;
-  const float* k_scale;
+  const float* k_scale;   // e4m3 pages, else NULL
   const float* v_scale;
+  const uint8_t* k_exp;   // e2m1 pages, else NULL: exponents, whose offset is the codes' / 16
+  const uint8_t* v_exp;
   int64_t page_stride;
   int32_t token_stride;   // a page spans less than 2 GiB, so offsets inside one fit 32 bits
   int32_t head_stride;
@@ -48,6 +50,24 @@ __device__ __forceinline__ int seq_of_row(const KvSeqs& s, int row) {
   return lo;
 }
 
+// Eight e4m3 codes of f / scale.
+__device__ __forceinline__ u32x2 codes_e4m3(const float (&x)[8], float scale) {
+  float f[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float v = x[e] / scale;
+    f[e] = v > 448.0f ? 448.0f : (v < -448.0f ? -448.0f : v);   // NaN stays NaN
+  }
+  u32x2 r;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    int b = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * w], f[4 * w + 1], 0, false);
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * w + 2], f[4 * w + 3], b, true);
+    r[w] = uint32_t(b);
+  }
+  return r;
+}
+
 struct AppendArgs {
   KvView c;
   KvSeqs s;
@@ -56,6 +76,24 @@ struct AppendArgs {
   int64_t row_stride;    // bytes
   int32_t head_stride;   // bytes
   int32_t rows;
+};
+
+constexpr int kRopeMaxAxes = 4;
+
+// Rotation of new rows, and the queries that are rotated beside them.
+struct RopeArgs {
+  const uint64_t* turns;   // of a frequency, in 2^-64 turns a position
+  const int32_t* positions;
+  int64_t position_stride;
+  const char* q;
+  char* q_out;
+  int64_t q_row_stride;    // bytes
+  int32_t q_head_stride;   // bytes
+  int32_t heads;
+  int32_t dim;             // rotated dimensions of a head; 0: none
+  int32_t interleaved;
+  float factor;
+  uint32_t axis[8];        // of a frequency, two bits each
 };
 
 struct EvictArgs {
@@ -195,16 +233,30 @@ constexpr int decode_wave_lds(int dim, int elem_bytes, int tile_rows) {
   const int out = tile_rows * (dim + 4) * 4;
   return ring > out ? ring : out;
 }
+// Over e2m1 pages: one step's values in 16 bits, and at the end the outputs.
+constexpr int decode4_wave_lds(int dim, int tile_rows) {
+  const int step = 2 * dim << kDecodeUnitShift, out = tile_rows * (dim + 4) * 4;
+  return step > out ? step : out;
+}
 // Decode blocks that share a CU's 160 KiB.
+constexpr int blocks_of_lds(int wave_lds) { return kDecodeWaves * wave_lds <= 76 * 1024 ? 2 : 1; }
 constexpr int decode_blocks(int dim, int elem_bytes, int tile_rows) {
-  return kDecodeWaves * decode_wave_lds(dim, elem_bytes, tile_rows) <= 76 * 1024 ? 2 : 1;
+  return blocks_of_lds(decode_wave_lds(dim, elem_bytes, tile_rows));
+}
+constexpr int decode4_blocks(int dim, int tile_rows) { return blocks_of_lds(decode4_wave_lds(dim, tile_rows)); }
+
+// Bytes of a position's keys (or values) of one head.
+constexpr int kv_row_bytes(int dim, int cache_dtype) {
+  return cache_dtype == LORA_KV_E2M1 ? dim / 2 + dim / 32 : (cache_dtype == LORA_KV_E4M3 ? dim : 2 * dim);
 }
 
 hipError_t launch_kv_append(const AppendArgs& a, int dtype, int cache_dtype, hipStream_t stream);
+hipError_t launch_kv_append_rope(const AppendArgs& a, const RopeArgs& r, int dtype, int cache_dtype, hipStream_t stream);
 hipError_t launch_kv_evict(const EvictArgs& a, int cache_dtype, hipStream_t stream);
 hipError_t launch_attn_prompt(const AttnArgs& a, const AttnPart& p, int dtype, int cache_dtype, hipStream_t stream);
 hipError_t launch_attn_decode(const AttnArgs& a, const AttnPart& p, int rows, int dtype, int cache_dtype,
                               hipStream_t stream);
+hipError_t launch_attn_decode4(const AttnArgs& a, const AttnPart& p, int rows, int dtype, hipStream_t stream);
 hipError_t launch_attn_join(const AttnArgs& a, const AttnPart& p, int tile_rows, int most, int dtype,
                             hipStream_t stream);
 // p.items: the launch's items, in seq[].item_end; sums of positions that several items share go to part_o.

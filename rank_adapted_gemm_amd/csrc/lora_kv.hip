@@ -21,18 +21,8 @@ __device__ __forceinline__ u32x2 to_e4m3(const u32x4& raw, float scale) {
   const vec8 x = __builtin_bit_cast(vec8, raw);
   float f[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float v = float(x[e]) / scale;
-    f[e] = v > 448.0f ? 448.0f : (v < -448.0f ? -448.0f : v);   // NaN stays NaN
-  }
-  u32x2 r;
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    int b = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * w], f[4 * w + 1], 0, false);
-    b = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * w + 2], f[4 * w + 3], b, true);
-    r[w] = uint32_t(b);
-  }
-  return r;
+  for (int e = 0; e < 8; ++e) f[e] = float(x[e]);
+  return codes_e4m3(f, scale);
 }
 
 // T: the rows' type; F8: the cache holds e4m3 codes.
@@ -381,7 +371,7 @@ constexpr int kGatherRows = 64;
 // Copies kept rows to their new slots, and their weights; blockIdx.y is the head, z the sequence (their
 // product may pass 65,535, which a dimension of a grid is documented to hold).  Bound by bytes:
 // 101 MB of 512-byte rows in 21 us (4.8 TB/s), 786 MB of 128-byte rows in 167 us (4.7 TB/s).
-__global__ __launch_bounds__(256) void evict_gather_kernel(EvictArgs a, int elem_bytes, uint32_t nan_word) {
+__global__ __launch_bounds__(256) void evict_gather_kernel(EvictArgs a, int row_bytes, uint32_t nan_word) {
   __shared__ int64_t src[kGatherRows], dst[kGatherRows];   // byte offsets; -1: no row, -2: source page invalid
   const int i = blockIdx.z, h = blockIdx.y;
   const int64_t pair = int64_t(i) * a.c.kv_heads + h;
@@ -410,7 +400,7 @@ __global__ __launch_bounds__(256) void evict_gather_kernel(EvictArgs a, int elem
           a.mass[pair * a.mass_cap + a.kept[pair * a.budget + slot]];
   }
   __syncthreads();
-  const int per = a.c.dim * elem_bytes / 16;
+  const int per = row_bytes / 16;   // e2m1: a byte of exponent for each
   for (int u = threadIdx.x; u < kGatherRows * per; u += 256) {
     const int r = u / per, c = (u - r * per) * 16;
     if (dst[r] < 0) continue;
@@ -421,6 +411,11 @@ __global__ __launch_bounds__(256) void evict_gather_kernel(EvictArgs a, int elem
     }
     *reinterpret_cast<u32x4*>(a.c.k + dst[r] + c) = kx;
     *reinterpret_cast<u32x4*>(a.c.v + dst[r] + c) = vx;
+    if (a.c.k_exp) {
+      const int64_t from = (src[r] + c) >> 4, to = (dst[r] + c) >> 4;
+      const_cast<uint8_t*>(a.c.k_exp)[to] = src[r] >= 0 ? a.c.k_exp[from] : 0xFF;
+      const_cast<uint8_t*>(a.c.v_exp)[to] = src[r] >= 0 ? a.c.v_exp[from] : 0xFF;
+    }
   }
 }
 
@@ -455,9 +450,10 @@ hipError_t launch_kv_evict(const EvictArgs& a, int cache_dtype, hipStream_t stre
     kept = n > kept ? n : kept;
   }
   if (kept == 0) return hipSuccess;
-  const bool f8 = cache_dtype == LORA_KV_E4M3;
+  const int row_bytes = a.c.dim * (cache_dtype == LORA_KV_E2M1 ? 1 : cache_dtype == LORA_KV_E4M3 ? 2 : 4) / 2;
+  const uint32_t nan_word = cache_dtype == LORA_KV_E2M1 ? 0u : cache_dtype == LORA_KV_E4M3 ? 0x7F7F7F7Fu : 0x7FFF7FFFu;
   hipLaunchKernelGGL(evict_gather_kernel, dim3((kept + kGatherRows - 1) / kGatherRows, a.c.kv_heads, a.s.n), dim3(256), 0,
-                     stream, a, f8 ? 1 : 2, f8 ? 0x7F7F7F7Fu : 0x7FFF7FFFu);
+                     stream, a, row_bytes, nan_word);
   return hipGetLastError();
 }
 
