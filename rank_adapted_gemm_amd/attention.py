@@ -126,21 +126,23 @@ class Rope:
         self._index = self._turns.get_device()
         self._axis = (ctypes.c_uint8 * half)(*axis)
 
-    def _struct(self, positions, rows):
-        """The library's rotation, and the tensor it points to kept beside it."""
+        self._c = _bd.RopeStruct(self._turns.data_ptr(), ctypes.cast(self._axis, ctypes.c_void_p), None, 0, self.axes,
+                                 self.dim, int(self.interleaved), self.factor)
+        self._ref = ctypes.byref(self._c)
+
+    def _at(self, positions, rows):
+        """The library's rotation with these positions."""
         import torch
-        at, stride, axes = None, 0, self.axes
-        if positions is not None:
-            if positions.dtype != torch.int32 or positions.get_device() != self._index or positions.dim() not in (1, 2):
-                raise ValueError("positions must be an int32 CUDA tensor (rows,) or (axes, rows) on the Rope's GPU")
-            if positions.shape[-1] != rows or (rows > 1 and positions.stride(-1) != 1):
-                raise ValueError(f"positions must hold the batch's {rows} rows, contiguous")
-            given = positions.shape[0] if positions.dim() == 2 else 1
-            if given < axes:
-                raise ValueError(f"positions hold {given} axes, the Rope takes {axes}")
-            at, stride = positions.data_ptr(), positions.stride(0) if positions.dim() == 2 and given > 1 else rows
-        return _bd.RopeStruct(self._turns.data_ptr(), ctypes.cast(self._axis, ctypes.c_void_p), at, stride, axes,
-                              self.dim, int(self.interleaved), self.factor)
+        if positions.dtype != torch.int32 or positions.get_device() != self._index or positions.dim() not in (1, 2):
+            raise ValueError("positions must be an int32 CUDA tensor (rows,) or (axes, rows) on the Rope's GPU")
+        given, stride = (positions.shape[0], positions.stride(0)) if positions.dim() == 2 else (1, 0)
+        if positions.shape[-1] != rows or (rows > 1 and positions.stride(-1) != 1):
+            raise ValueError(f"positions must hold the batch's {rows} rows, contiguous")
+        if given < self.axes:
+            raise ValueError(f"positions hold {given} axes, the Rope takes {self.axes}")
+        c = _bd.RopeStruct.from_buffer_copy(self._c)   # of this call's own: other threads may make theirs
+        c.positions, c.position_stride = positions.data_ptr(), stride
+        return ctypes.byref(c)
 
 
 class KVBatch:
@@ -261,22 +263,23 @@ def kv_append(cache, batch, k, v, rope=None, positions=None, q=None, q_out=None,
         return None
     if rope._index != cache._index:
         raise ValueError(f"the Rope is on GPU {rope._index}, the cache on {cache.device}")
-    turn = rope._struct(positions, batch.rows)
+    turn = rope._ref if positions is None else rope._at(positions, batch.rows)
     s = _handle(stream, cache)
-    heads, q_strides, q_at, out_at = 0, (0, 0), None, None
-    if q is not None:
-        if code != _row_code(cache, batch, "q", q):
-            raise ValueError("q must be of the type of k and v")
-        q_strides, heads, q_at = _strides3("q", q, cache.head_dim), q.shape[1], q.data_ptr()
-        if q_out is None:
-            q_out = _empty(q.shape, q.dtype, cache.device, stream)
-        elif q_out.dtype != q.dtype or q_out.device != cache.device or not q_out.is_contiguous() or q_out.shape != q.shape:
-            raise ValueError("q_out must be a contiguous tensor like q")
-        out_at = q_out.data_ptr()
-    elif q_out is not None:
-        raise ValueError("q_out goes with q")
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out goes with q")
+        _call(cache, _bd.load().lora_kv_append_rope, cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), strides[0],
+              strides[1], code, turn, None, 0, 0, 0, None, s)
+        return None
+    if code != _row_code(cache, batch, "q", q):
+        raise ValueError("q must be of the type of k and v")
+    q_row, q_head = _strides3("q", q, cache.head_dim)
+    if q_out is None:
+        q_out = _empty(q.shape, q.dtype, cache.device, stream)
+    elif q_out.dtype != q.dtype or q_out.get_device() != cache._index or not q_out.is_contiguous() or q_out.shape != q.shape:
+        raise ValueError("q_out must be a contiguous tensor like q")
     _call(cache, _bd.load().lora_kv_append_rope, cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), strides[0],
-          strides[1], code, ctypes.byref(turn), q_at, q_strides[0], q_strides[1], heads, out_at, s)
+          strides[1], code, turn, q.data_ptr(), q_row, q_head, q.shape[1], q_out.data_ptr(), s)
     return q_out
 
 
