@@ -52,12 +52,10 @@ struct ValueReader16 {
 // number of the call, which no other call has, and is cleared by the join, so that the same launch may run
 // again from a graph.  Two items may both find the row complete; they write the same values.  Sums and
 // marks go past the XCD's L2 (device scope): the other items run on other XCDs.
-template <typename T, int DIM>
-__device__ __forceinline__ void join_last(const AttnArgs& a, const AttnSeq& sq, int first, int head, int tile_rows, int M,
-                                          float vs, float* lds) {
+
+// Whether this item found them all; `arrived`: of the row's first split, the others a head count apart.
+__device__ __forceinline__ bool all_arrived(const AttnArgs& a, const AttnSeq& sq, const uint64_t* arrived) {
   const int tid = threadIdx.x;
-  uint64_t* arrived = a.arrived + first + head;   // of the row's first split; the others a head count apart
-  const int64_t slot0 = (int64_t(first) + head) * tile_rows, step = int64_t(a.c.kv_heads) * tile_rows;
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
   __syncthreads();                                // every thread's sums are where the others will look
   if (tid == 0)
@@ -67,7 +65,21 @@ __device__ __forceinline__ void join_last(const AttnArgs& a, const AttnSeq& sq, 
   bool missing = false;
   for (int i = tid; i < sq.nsplit; i += kDecodeWaves * 64)
     missing |= __hip_atomic_load(arrived + int64_t(i) * a.c.kv_heads, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != a.call;
-  if (__syncthreads_or(missing)) return;
+  return !__syncthreads_or(missing);
+}
+
+__device__ __forceinline__ void clear_arrived(const AttnArgs& a, const AttnSeq& sq, uint64_t* arrived) {
+  for (int i = threadIdx.x; i < sq.nsplit; i += kDecodeWaves * 64)
+    __hip_atomic_store(arrived + int64_t(i) * a.c.kv_heads, uint64_t(0), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+template <typename T, int DIM>
+__device__ __forceinline__ void join_last(const AttnArgs& a, const AttnSeq& sq, int first, int head, int tile_rows, int M,
+                                          float vs, float* lds) {
+  const int tid = threadIdx.x;
+  uint64_t* arrived = a.arrived + first + head;   // of the row's first split; the others a head count apart
+  const int64_t slot0 = (int64_t(first) + head) * tile_rows, step = int64_t(a.c.kv_heads) * tile_rows;
+  if (!all_arrived(a, sq, arrived)) return;
   const uint32_t span = uint32_t((sq.nsplit - 1) * step + tile_rows);
   const auto po = make_rsrc(a.part_o + slot0 * DIM, span * DIM * 4), pm = make_rsrc(a.part_ml + slot0 * 2, span * 8);
   // maxima and sums of all rows and splits
@@ -104,64 +116,149 @@ __device__ __forceinline__ void join_last(const AttnArgs& a, const AttnSeq& sq, 
     *reinterpret_cast<u32x2*>(a.out + (row * DIM + d) * 2) =
         u32x2{pack_pair<T>(acc[0] * inv, acc[1] * inv), pack_pair<T>(acc[2] * inv, acc[3] * inv)};
   }
-  for (int i = tid; i < sq.nsplit; i += kDecodeWaves * 64)
-    __hip_atomic_store(arrived + int64_t(i) * a.c.kv_heads, uint64_t(0), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  clear_arrived(a, sq, arrived);
 }
 
-// The waves' rows meet in LDS, WAVE_LDS bytes a wave, and leave for the output, or where they were split for the workspace.
-template <typename T, int DIM, int QT, bool MASS, int WAVE_LDS>
+template <typename T, int DIM>
+__device__ __forceinline__ void store_joined(const AttnArgs& a, const AttnSeq& sq, int head, int m, int d, f32x4 acc, float total) {
+  const float inv = total == 0 ? 0.0f : 1.0f / total;
+  const int j = m / a.group;
+  const int64_t row = int64_t(sq.q_start + j) * a.heads + (m - j * a.group) + head * a.group;
+  *reinterpret_cast<u32x2*>(a.out + (row * DIM + d) * 2) =
+      u32x2{pack_pair<T>(acc[0] * inv, acc[1] * inv), pack_pair<T>(acc[2] * inv, acc[3] * inv)};
+}
+
+// The same for many short items: a row's factors once, by sixteen lanes, eight or sixteen of its sums under way a thread, and
+// where there are threads to spare several share a row's splits, whose parts meet in LDS.
+template <typename T, int DIM>
+__device__ __forceinline__ void join_many(const AttnArgs& a, const AttnSeq& sq, int first, int head, int tile_rows, int M,
+                                          float* lds) {
+  constexpr int DEPTH = DIM == 256 ? 16 : 8;
+  const int tid = threadIdx.x, ns = sq.nsplit;
+  uint64_t* arrived = a.arrived + first + head;
+  const int64_t slot0 = (int64_t(first) + head) * tile_rows, step = int64_t(a.c.kv_heads) * tile_rows;
+  if (!all_arrived(a, sq, arrived)) return;
+  const uint32_t span = uint32_t((ns - 1) * step + tile_rows);
+  const auto po = make_rsrc(a.part_o + slot0 * DIM, span * DIM * 4), pm = make_rsrc(a.part_ml + slot0 * 2, span * 8);
+  // each row's sum; its splits' maxima, then their factors; their sums, then parts of outputs
+  float *sums = lds, *factor = sums + kAttnDecodeMaxRows, *parts = factor + (M * ns + 3) / 4 * 4;
+  for (int z = tid; z < M * ns; z += kDecodeWaves * 64) {
+    const int m = z / ns, i = z - m * ns;
+    const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(pm, uint32_t(m + i * step) * 8, 0, kDeviceScope);
+    factor[z] = __builtin_bit_cast(float, uint32_t(x[0]));
+    parts[z] = __builtin_bit_cast(float, uint32_t(x[1]));
+  }
+  __syncthreads();
+  for (int m = tid >> 4; m < M; m += kDecodeWaves * 4) {   // sixteen lanes a row
+    float top = kLowest, total = 0;
+    for (int i = tid & 15; i < ns; i += 16) top = __builtin_fmaxf(top, factor[m * ns + i]);
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
+    for (int i = tid & 15; i < ns; i += 16) {
+      const float f = __builtin_amdgcn_exp2f(factor[m * ns + i] - top);
+      factor[m * ns + i] = f;
+      total += f * parts[m * ns + i];
+    }
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) total += __shfl_xor(total, d);
+    if ((tid & 15) == 0) sums[m] = total;
+  }
+  __syncthreads();
+  const int cells = M * (DIM / 4), groups = cells >= kDecodeWaves * 64 ? 1 : kDecodeWaves * 64 / cells;
+  const int group = groups == 1 ? 0 : tid / cells;
+  for (int z = groups == 1 ? tid : tid - group * cells; z < cells && group < groups; z += kDecodeWaves * 64) {
+    const int m = z / (DIM / 4), d = (z - m * (DIM / 4)) * 4;
+    f32x4 acc = {0, 0, 0, 0};
+    for (int i0 = group; i0 < ns; i0 += DEPTH * groups) {
+      f32x4 o[DEPTH];
+      float f[DEPTH];
+#pragma unroll
+      for (int n = 0; n < DEPTH; ++n) {
+        const int i = min(i0 + n * groups, ns - 1);
+        o[n] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(po, (uint32_t(m + i * step) * DIM + d) * 4, 0, kDeviceScope));
+        f[n] = factor[m * ns + i];
+      }
+#pragma unroll
+      for (int n = 0; n < DEPTH; ++n)
+        if (i0 + n * groups < ns) acc += o[n] * f[n];
+    }
+    if (groups > 1) *reinterpret_cast<f32x4*>(parts + (group * cells + z) * 4) = acc;
+    else store_joined<T, DIM>(a, sq, head, m, d, acc, sums[m]);
+  }
+  if (groups > 1) {
+    __syncthreads();
+    if (tid < cells) {
+      f32x4 acc = *reinterpret_cast<const f32x4*>(parts + tid * 4);
+      for (int g = 1; g < groups; ++g) acc += *reinterpret_cast<const f32x4*>(parts + (g * cells + tid) * 4);
+      const int m = tid / (DIM / 4);
+      store_joined<T, DIM>(a, sq, head, m, (tid - m * (DIM / 4)) * 4, acc, sums[m]);
+    }
+  }
+  clear_arrived(a, sq, arrived);
+}
+
+// The waves' rows meet in LDS, WAVE_LDS bytes a wave, in RUNS runs of their columns, and leave for the output, or where they
+// were split for the workspace.
+template <typename T, int DIM, int QT, bool MASS, int WAVE_LDS, int RUNS = 1, bool MANY = false>
 __device__ __forceinline__ void meet_waves(const AttnArgs& a, const AttnSeq& sq, int first, int head, int M, float vs, char* lds,
                                            float (&ml)[kDecodeWaves][QT * 16][2], const f32x4 (&o)[QT][DIM / 16],
                                            const float (&top)[QT], const float (&total)[QT]) {
-  constexpr int BM = QT * 16, DB = DIM / 16;
+  constexpr int BM = QT * 16, W = DIM / RUNS, DB = W / 16;
+  static_assert(WAVE_LDS >= BM * (W + 4) * 4, "a wave's outputs");
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int qd = lane >> 4, col = lane & 15;
   float* mo = reinterpret_cast<float*>(lds + wave * WAVE_LDS);
-#pragma unroll
-  for (int x = 0; x < QT; ++x) {
-    if (x * 16 + col < M) {
-#pragma unroll
-      for (int d = 0; d < DB; ++d)
-        *reinterpret_cast<f32x4*>(mo + (x * 16 + col) * (DIM + 4) + d * 16 + qd * 4) = o[x][d];
-    }
-    if (qd == 0) {
-      ml[wave][x * 16 + col][0] = top[x];
-      ml[wave][x * 16 + col][1] = total[x];
-    }
-  }
-  __syncthreads();
   const auto po = make_rsrc(a.part_o + int64_t(blockIdx.x) * BM * DIM, BM * DIM * 4);
   const auto pm = make_rsrc(a.part_ml + int64_t(blockIdx.x) * BM * 2, BM * 8);
-  for (int z = tid; z < M * (DIM / 4); z += kDecodeWaves * 64) {
-    const int m = z / (DIM / 4), d = (z - m * (DIM / 4)) * 4;
-    float best = ml[0][m][0];
 #pragma unroll
-    for (int y = 1; y < kDecodeWaves; ++y) best = __builtin_fmaxf(best, ml[y][m][0]);
-    float total = 0;
-    f32x4 acc = {0, 0, 0, 0};
+  for (int run = 0; run < RUNS; ++run) {
+    if (run > 0) __syncthreads();
 #pragma unroll
-    for (int y = 0; y < kDecodeWaves; ++y) {
-      const float f = __builtin_amdgcn_exp2f(ml[y][m][0] - best);
-      total += ml[y][m][1] * f;
-      acc += *reinterpret_cast<const f32x4*>(lds + y * WAVE_LDS + (m * (DIM + 4) + d) * 4) * f;
+    for (int x = 0; x < QT; ++x) {
+      if (x * 16 + col < M) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+          *reinterpret_cast<f32x4*>(mo + (x * 16 + col) * (W + 4) + d * 16 + qd * 4) = o[x][run * DB + d];
+      }
+      if (run == 0 && qd == 0) {
+        ml[wave][x * 16 + col][0] = top[x];
+        ml[wave][x * 16 + col][1] = total[x];
+      }
     }
-    if (sq.nsplit > 1) {
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc), po, uint32_t(m * DIM + d) * 4, 0, kDeviceScope);
-      if (d == 0)
-        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, f32x2{best, total}), pm, uint32_t(m) * 8, 0,
-                                              kDeviceScope);
-    } else {
-      const float inv = total == 0 ? 0.0f : vs / total;
-      const int j = m / a.group;
-      const int64_t row = int64_t(sq.q_start + j) * a.heads + (m - j * a.group) + head * a.group;
-      *reinterpret_cast<u32x2*>(a.out + (row * DIM + d) * 2) =
-          u32x2{pack_pair<T>(acc[0] * inv, acc[1] * inv), pack_pair<T>(acc[2] * inv, acc[3] * inv)};
-      // accumulated weights are taken against these, also where the rows were not split
-      if (MASS && d == 0) *reinterpret_cast<f32x2*>(a.part_ml + (int64_t(blockIdx.x) * BM + m) * 2) = f32x2{best, total};
+    __syncthreads();
+    for (int z = tid; z < M * (W / 4); z += kDecodeWaves * 64) {
+      const int m = z / (W / 4), d = (z - m * (W / 4)) * 4, to = run * W + d;
+      float best = ml[0][m][0];
+#pragma unroll
+      for (int y = 1; y < kDecodeWaves; ++y) best = __builtin_fmaxf(best, ml[y][m][0]);
+      float total = 0;
+      f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+      for (int y = 0; y < kDecodeWaves; ++y) {
+        const float f = __builtin_amdgcn_exp2f(ml[y][m][0] - best);
+        total += ml[y][m][1] * f;
+        acc += *reinterpret_cast<const f32x4*>(lds + y * WAVE_LDS + (m * (W + 4) + d) * 4) * f;
+      }
+      if (sq.nsplit > 1) {
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc), po, uint32_t(m * DIM + to) * 4, 0, kDeviceScope);
+        if (to == 0)
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, f32x2{best, total}), pm, uint32_t(m) * 8, 0,
+                                                kDeviceScope);
+      } else {
+        const float inv = total == 0 ? 0.0f : vs / total;
+        const int j = m / a.group;
+        const int64_t row = int64_t(sq.q_start + j) * a.heads + (m - j * a.group) + head * a.group;
+        *reinterpret_cast<u32x2*>(a.out + (row * DIM + to) * 2) =
+            u32x2{pack_pair<T>(acc[0] * inv, acc[1] * inv), pack_pair<T>(acc[2] * inv, acc[3] * inv)};
+        // accumulated weights are taken against these, also where the rows were not split
+        if (MASS && to == 0) *reinterpret_cast<f32x2*>(a.part_ml + (int64_t(blockIdx.x) * BM + m) * 2) = f32x2{best, total};
+      }
     }
   }
   if constexpr (!MASS) {
-    if (a.arrived && sq.nsplit > 1) join_last<T, DIM>(a, sq, first, head, BM, M, vs, reinterpret_cast<float*>(lds));
+    if (!a.arrived || sq.nsplit == 1) return;
+    if constexpr (MANY) join_many<T, DIM>(a, sq, first, head, BM, M, reinterpret_cast<float*>(lds));
+    else join_last<T, DIM>(a, sq, first, head, BM, M, vs, reinterpret_cast<float*>(lds));
   }
 }
 

@@ -1,4 +1,22 @@
 // Attention of single tokens (and few rows) over e2m1 pages.
+//
+// As over other pages a block takes the packed rows of one sequence and key-value head and a run of its positions, and
+// its four waves 32 positions each in turn; sums are the same, S^T = K Q^T and O^T = V^T P^T on 16 x 16 x 32 MFMAs.  What
+// differs is what bounds it: a position is 4.25 bits a value, so that turning codes into T costs about as much as
+// streaming them (one conversion, v_cvt_scalef32_pk, makes two values and applies their block's power of two; it runs at
+// the rate of any other vector instruction).  Hence:
+//   - codes go from memory to registers, which hold what is under way; keys' are refilled once they are multiplied,
+//     values' once they are in LDS, so that either has about a step to arrive, and four blocks share a CU (two at
+//     256-wide heads).  A loop over several steps' registers was measured: the compiler gave every step outputs of its
+//     own, 60 registers a step, and copied them (64 streams 158 us with two steps and two blocks).
+//   - a block of 32 values is 16 bytes, a lane's load, and shares a scale: a key fragment is four products' operands.
+//   - V has to be read in columns, while its scales lie along rows, so a wave turns its values into T row by row, in
+//     its own tile of LDS, and reads that with the transposing reads.  256-wide heads go by in two halves, which halves
+//     the tile, and keep their queries in LDS.
+//
+// Measured, a call with inputs that the caches do not hold: 64 streams of 4,099 - 16,132 positions, 8 heads of 128, 705 MB
+// of codes and scales in 140 us (5.0 TB/s; the same over e4m3 pages 267); six chats, 4 heads of 256, 90 MB in 30 us,
+// of which 10.5 are what a call of 310 positions takes (over 16-bit pages 68 and 12).
 #include "lora_attn_decode.h"
 
 namespace lora {
@@ -7,25 +25,33 @@ namespace {
 constexpr int kStep = 1 << kDecodeUnitShift;
 constexpr int kWaves = kDecodeWaves;
 
-// A lane's codes of one load: a block, or half of one at 64-wide heads.
+// A lane's codes of 16 positions in a run of DIM dimensions: a block, or half of one where those are 64.
 template <int DIM>
 struct Codes {
   static constexpr int kBytes = DIM == 64 ? 8 : 16, kWords = kBytes / 4;
-  static constexpr int kRowLanes = DIM / 2 / kBytes;        // lanes of a row
-  static constexpr int kLoads = 16 * kRowLanes / 64;        // loads of a 16-row group
+  static constexpr int kRowLanes = DIM / 2 / kBytes;        // lanes of a row: four
   typedef uint32_t words __attribute__((ext_vector_type(kWords)));
 };
+
+template <typename C>
+__device__ __forceinline__ typename C::words load_codes(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  if constexpr (C::kWords == 4) return __builtin_bit_cast(typename C::words, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+  else return __builtin_bit_cast(typename C::words, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+}
 
 // QT: 16-row columns of packed rows.  MASS: scores go to the workspace.
 template <typename T, int DIM, int QT, bool MASS>
 __global__ __launch_bounds__(kWaves * 64, decode4_blocks(DIM, QT * 16)) void decode4_kernel(AttnArgs a, AttnPart part) {
-  using R = Row<false, DIM>;   // of the values once they are T
-  using C = Codes<DIM>;
+  constexpr int HALVES = decode4_halves(DIM), HD = DIM / HALVES;   // a step's dimensions go by in runs of HD
+  using R = Row<false, HD>;    // of the values once they are T
+  using Q = Row<false, DIM>;   // of the queries in LDS
+  using C = Codes<HD>;
   using x8 = typename Vec<T>::x8;
-  constexpr int BM = QT * 16, KS = DIM / 32, DB = DIM / 16;
-  constexpr int NS = DIM * QT >= 256 ? 1 : 2;               // steps under way
+  constexpr int BM = QT * 16, KH = HD / 32, DH = HD / 16, DB = DIM / 16;
+  constexpr bool QLDS = HALVES > 1;   // registers are short there
   constexpr int WAVE_LDS = decode4_wave_lds(DIM, BM);
   __shared__ __attribute__((aligned(1024))) char lds[kWaves * WAVE_LDS];
+  __shared__ __attribute__((aligned(16))) char qlds[QLDS ? BM * Q::kBytes : 16];
   __shared__ float ml[kWaves][BM][2];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -59,45 +85,47 @@ __global__ __launch_bounds__(kWaves * 64, decode4_blocks(DIM, QT * 16)) void dec
       place_hi[g] = page >= 0 ? int32_t(at >> 32) : (page == -1 ? -2 : -1);
     }
   };
-  // A step's codes and exponents.  Keys: lane's position col, dimensions 32 (or 16) qd on; values: a row after
-  // the other, the lanes' blocks side by side.
-  struct Step {
-    typename C::words k[2][C::kLoads], v[2][C::kLoads];
-    uint32_t ke[2][C::kLoads], ve[2][C::kLoads];
-    uint32_t bad;   // invalid groups, a bit each
-  };
-  const uint32_t ts = uint32_t(a.c.token_stride), te = ts >> 4;
+  // A step's codes and exponents.  Keys: lane's position col, 32 (or 16) dimensions from qd's on; values: a row
+  // after the other, the lanes' blocks side by side.
+  typename C::words kc[HALVES][2], vc[HALVES][2];
+  uint32_t ke[HALVES][2], ve[HALVES][2];
+  uint32_t badk = 0;   // of the step whose keys these are: invalid groups, a bit each
+  const uint32_t ts = uint32_t(a.c.token_stride), te = ts >> 4, group_bytes = 15 * ts + DIM / 2;
   const int vrow = lane / C::kRowLanes, vpart = lane % C::kRowLanes;
   const uint32_t kcode = uint32_t(col) * ts + uint32_t(qd) * C::kBytes, kexp = uint32_t(col) * te + uint32_t(qd * C::kBytes >> 4);
   const uint32_t vcode = uint32_t(vrow) * ts + uint32_t(vpart) * C::kBytes, vexp = uint32_t(vrow) * te + uint32_t(vpart * C::kBytes >> 4);
-  auto issue = [&](Step& st, int i) {
-    st.bad = 0;
+  // A step's groups in one of the pools.  Nowhere: loads through a descriptor without bytes give zeros.
+  struct Aim {
+    __amdgpu_buffer_rsrc_t codes[2], exps[2];
+    uint32_t bad;
+  };
+  auto aim = [&](int i, const char* codes, const uint8_t* exps) {
+    Aim r;
+    r.bad = 0;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const int hi = __builtin_amdgcn_readlane(place_hi[g], i & 63);
       const uint32_t lo = uint32_t(__builtin_amdgcn_readlane(place_lo[g], i & 63));
-      st.bad |= (hi == -2 ? 1u : 0u) << g;
-      // nowhere: the pool's first rows, which nothing is made of
-      const int64_t at = hi >= 0 && i < mine ? int64_t(hi) << 32 | lo : 0;
-      const char *kp = a.c.k + at, *vp = a.c.v + at;
-      const uint8_t *kx = a.c.k_exp + (at >> 4), *vx = a.c.v_exp + (at >> 4);
+      const bool there = hi >= 0 && i < mine;
+      const int64_t at = there ? int64_t(hi) << 32 | lo : 0;
+      const uint32_t bytes = there ? group_bytes : 0u;
+      r.codes[g] = make_rsrc(codes + at, bytes);
+      r.exps[g] = make_rsrc(exps + (at >> 4), bytes >> 4);
+      r.bad |= hi == -2 ? 1u << g : 0u;
+    }
+    return r;
+  };
+  auto fill = [&](const Aim& r, int h, uint32_t code, uint32_t exp, typename C::words (&c)[2], uint32_t (&e)[2]) {
 #pragma unroll
-      for (int n = 0; n < C::kLoads; ++n) {
-        st.k[g][n] = *reinterpret_cast<const typename C::words*>(kp + (kcode + n * 64));
-        st.ke[g][n] = kx[kexp + n * 4];
-      }
-#pragma unroll
-      for (int n = 0; n < C::kLoads; ++n) {
-        const uint32_t rows = uint32_t(n * (16 / C::kLoads)) * ts;
-        st.v[g][n] = *reinterpret_cast<const typename C::words*>(vp + (vcode + rows));
-        st.ve[g][n] = vx[vexp + (rows >> 4)];
-      }
+    for (int g = 0; g < 2; ++g) {
+      c[g] = load_codes<C>(r.codes[g], code + h * 64);
+      e[g] = __builtin_amdgcn_raw_buffer_load_b8(r.exps[g], exp + h * 4, 0, 0);
     }
   };
 
   // queries: the second operand, lane's packed row col, 8 of its dimensions a product
   int t[QT], low[QT];
-  x8 q[QT][KS];
+  x8 q[QT][QLDS ? 1 : KH];
   const float sc = a.scale * kLog2e;
   const uint32_t flip = sc < 0 ? 0x80008000u : 0u;                               // the scale's sign, exactly
   const float c = __builtin_fmaxf(__builtin_fabsf(sc), 1.17549435e-38f);         // not 0: hidden scores are -inf
@@ -108,16 +136,39 @@ __global__ __launch_bounds__(kWaves * 64, decode4_blocks(DIM, QT * 16)) void dec
     t[i] = m < M ? t0 + j : -1;
     low[i] = a.window < 0 ? 0 : t[i] - a.window + 1;
     const char* src = a.q + (sq.q_start + j) * a.q_row_stride + int64_t(h) * a.q_head_stride;
+    if constexpr (QLDS) {   // a quarter of each row's chunks a wave
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const int d = (k / C::kWords) * 128 + qd * C::kBytes * 2 + (k % C::kWords) * 8;
-      q[i][k] = __builtin_bit_cast(x8, *reinterpret_cast<const u32x4*>(src + d * 2) ^ flip);
+      for (int n = 0; n < Q::kChunks / 16; ++n) {
+        const int chunk = wave * (Q::kChunks / 4) + qd * (Q::kChunks / 16) + n;
+        *reinterpret_cast<u32x4*>(qlds + (i * 16 + col) * Q::kBytes + ((chunk ^ Q::key_swizzle(col)) << 4)) =
+            *reinterpret_cast<const u32x4*>(src + chunk * 16) ^ flip;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < KH; ++k)
+        q[i][k] = __builtin_bit_cast(x8, *reinterpret_cast<const u32x4*>(src + (qd * C::kBytes * 2 + k * 8) * 2) ^ flip);
     }
   }
   load_pages(0);
-  Step ring[NS];
+  // Codes are refilled once they were used, so that each run has about a step to arrive.
+  {
+    const Aim ka = aim(0, a.c.k, a.c.k_exp), va = aim(0, a.c.v, a.c.v_exp);
+    badk = ka.bad;
 #pragma unroll
-  for (int n = 0; n < NS; ++n) issue(ring[n], n);
+    for (int h = 0; h < HALVES; ++h) fill(ka, h, kcode, kexp, kc[h], ke[h]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h) fill(va, h, vcode, vexp, vc[h], ve[h]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if constexpr (QLDS) __syncthreads();
+  const char* qbase = qlds + col * Q::kBytes;
+  auto query = [&](int x, int h, int k) {
+    if constexpr (QLDS)
+      return *reinterpret_cast<const x8*>(qbase + x * 16 * Q::kBytes + (((h * 16 + qd * 4 + k) ^ Q::key_swizzle(col)) << 4));
+    else
+      return q[x][k];
+  };
   f32x4 o[QT][DB];
   float top[QT], sum[QT];
 #pragma unroll
@@ -128,32 +179,41 @@ __global__ __launch_bounds__(kWaves * 64, decode4_blocks(DIM, QT * 16)) void dec
     for (int d = 0; d < DB; ++d) o[i][d] = f32x4{0, 0, 0, 0};
   }
   const uint32_t tile = lds_addr(lds) + wave * WAVE_LDS;
-  const ValueReader16<T, false, DIM> vr(lane);
+  const ValueReader16<T, false, HD> vr(lane);
   const uint32_t vwrite = tile + uint32_t(vrow * R::kBytes) +
-                          (uint32_t((vpart * C::kWords) ^ ValueReader16<T, false, DIM>::swizzle(vrow)) << 4);
+                          (uint32_t((vpart * C::kWords) ^ ValueReader16<T, false, HD>::swizzle(vrow)) << 4);
   float* scores = nullptr;
   const int score_row = score_steps(units, sq.nsplit) * kStep;
   if constexpr (MASS)
     scores = a.scores + int64_t(sq.score) * kStep + ((int64_t(blockIdx.x) - first) * M + col) * score_row + qd * 4;
   bool again = false;
 
-  auto step = [&](Step& r, int i) {
+  for (int i = 0; i < mine; ++i) {
     const int p0 = units.unit(u0 + wave + i * kWaves) * kStep;
-    const uint32_t badp = r.bad;
+    const uint32_t badp = badk;
+    if (((i + 1) & 63) == 0) load_pages(i + 1);
     f32x4 st[QT][2];
+    {
+      const Aim next = aim(i + 1, a.c.k, a.c.k_exp);
+      badk = next.bad;
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
+      for (int h = 0; h < HALVES; ++h) {
 #pragma unroll
-      for (int x = 0; x < QT; ++x) st[x][g] = f32x4{0, 0, 0, 0};
+        for (int g = 0; g < 2; ++g) {
+          const float scale = scale_of(ke[h][g]);
 #pragma unroll
-      for (int n = 0; n < C::kLoads; ++n) {
-        const float scale = scale_of(r.ke[g][n]);
+          for (int x = 0; x < QT; ++x)
+            if (h == 0) st[x][g] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < C::kWords; ++k) {
-          const x8 kf = from_e2m1<T>(r.k[g][n][k], scale);
+          for (int k = 0; k < KH; ++k) {
+            const x8 kf = from_e2m1<T>(kc[h][g][k], scale);
 #pragma unroll
-          for (int x = 0; x < QT; ++x) st[x][g] = mfma16<T>(kf, q[x][n * C::kWords + k], st[x][g]);
+            for (int x = 0; x < QT; ++x) st[x][g] = mfma16<T>(kf, query(x, h, k), st[x][g]);
+          }
         }
+        __builtin_amdgcn_sched_barrier(0);
+        fill(next, h, kcode, kexp, kc[h], ke[h]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     const bool masked = badp != 0 ||
@@ -176,10 +236,10 @@ __global__ __launch_bounds__(kWaves * 64, decode4_blocks(DIM, QT * 16)) void dec
 #pragma unroll
       for (int g = 0; g < 2; ++g)
 #pragma unroll
-        for (int n = 0; n < C::kLoads; ++n) {
-          const int p = p0 + g * 16 + n * (16 / C::kLoads) + vrow;
-          if (r.ve[g][n] < kFirstInfinite<T>) continue;
-          r.ve[g][n] = 0;
+        for (int h = 0; h < HALVES; ++h) {
+          const int p = p0 + g * 16 + vrow;
+          if (ve[h][g] < kFirstInfinite<T>) continue;
+          ve[h][g] = 0;
           seen |= p <= t_hi && (p >= pages.lo_pos || p < a.sinks);
         }
       again |= __any(seen);
@@ -227,36 +287,31 @@ __global__ __launch_bounds__(kWaves * 64, decode4_blocks(DIM, QT * 16)) void dec
     // values: T in the wave's tile, a lane's block after the other's, then read in columns.  A wave's LDS accesses
     // are done in order.
     typedef __attribute__((address_space(3))) u32x4* p16;
+    const Aim next = aim(i + 1, a.c.v, a.c.v_exp);
 #pragma unroll
-    for (int g = 0; g < 2; ++g)
+    for (int h = 0; h < HALVES; ++h) {
 #pragma unroll
-      for (int n = 0; n < C::kLoads; ++n) {
-        const float scale = scale_of(r.ve[g][n]);
+      for (int g = 0; g < 2; ++g) {
+        const float scale = scale_of(ve[h][g]);
 #pragma unroll
         for (int k = 0; k < C::kWords; ++k)
-          *p16(uintptr_t((vwrite ^ uint32_t(k << 4)) + (g * 16 + n * (16 / C::kLoads)) * R::kBytes)) =
-              __builtin_bit_cast(u32x4, from_e2m1<T>(r.v[g][n][k], scale));
+          *p16(uintptr_t((vwrite ^ uint32_t(k << 4)) + g * 16 * R::kBytes)) =
+              __builtin_bit_cast(u32x4, from_e2m1<T>(vc[h][g][k], scale));
       }
-    if (((i + NS) & 63) == 0) load_pages(i + NS);
-    issue(r, i + NS);
-    asm volatile("" : : : "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      fill(next, h, vcode, vexp, vc[h], ve[h]);
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" : : : "memory");
 #pragma unroll
-    for (int d = 0; d < DB; ++d) {
-      const x8 vf = __builtin_bit_cast(x8, vr.read(tile, d));
+      for (int d = 0; d < DH; ++d) {
+        const x8 vf = __builtin_bit_cast(x8, vr.read(tile, d));
 #pragma unroll
-      for (int x = 0; x < QT; ++x) o[x][d] = mfma16<T>(vf, rest[x], mfma16<T>(vf, w[x], o[x][d]));
-    }
-    asm volatile("" : : : "memory");
-  };
-  // Every step is left for the next one or for good, so that the compiler's waits count the steps under way.
-  for (int i = 0;; i += NS) {
-#pragma unroll
-    for (int n = 0; n < NS; ++n) {
-      if (i + n >= mine) goto done;
-      step(ring[n], i + n);
+        for (int x = 0; x < QT; ++x)
+          o[x][h * DH + d] = mfma16<T>(vf, rest[x], mfma16<T>(vf, w[x], o[x][h * DH + d]));
+      }
+      asm volatile("" : : : "memory");
     }
   }
-done:
 
   // An infinite value takes weights only, as over other pages.
   float total[QT];
@@ -277,11 +332,11 @@ done:
                                     sq.nsplit > 1 || MASS ? int64_t(blockIdx.x) * BM + m : -1);
     if constexpr (!MASS) {
       __threadfence();   // rows of slow_row lie in this XCD's L2
-      if (a.arrived && sq.nsplit > 1) join_last<T, DIM>(a, sq, first, item.head, BM, M, 1.0f, reinterpret_cast<float*>(lds));
+      if (a.arrived && sq.nsplit > 1) join_many<T, DIM>(a, sq, first, item.head, BM, M, reinterpret_cast<float*>(lds));
     }
     return;
   }
-  meet_waves<T, DIM, QT, MASS, WAVE_LDS>(a, sq, first, item.head, M, 1.0f, lds, ml, o, top, total);
+  meet_waves<T, DIM, QT, MASS, WAVE_LDS, HALVES, true>(a, sq, first, item.head, M, 1.0f, lds, ml, o, top, total);
 }
 
 template <typename T, int DIM, int QT>

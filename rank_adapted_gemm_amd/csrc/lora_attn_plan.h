@@ -98,10 +98,11 @@ struct AttnDeal {
 };
 
 // The longest run of units an item may take, so that the launch ends soonest.  `each` and `split` are what
-// an item and what leaving sums in the workspace cost in units, `join` the join's launch.  `shared`: what a
-// unit costs where two items share a slot, 0 where they cannot; few items have the slots to themselves.
+// an item and what leaving sums in the workspace cost in units, `join` the join's launch and `joined` what it
+// takes for each split of a row.  `shared`: what a unit costs where two items share a slot, 0 where they
+// cannot; few items have the slots to themselves.
 inline int attn_chunk(const AttnWork* w, int n, int64_t kv_heads, int64_t slots, double each, double split,
-                      double join, int least, double shared) {
+                      double join, double joined, int least, double shared) {
   constexpr int kClasses = 12;   // sequences of similar length count as one class
   struct Class {
     double last, first;
@@ -127,11 +128,11 @@ inline int attn_chunk(const AttnWork* w, int n, int64_t kv_heads, int64_t slots,
   double best_cost = 0;
   for (int c = top;; c = std::max(least, int(c * 0.86))) {
     AttnDeal deal;
-    bool any = false;
+    int64_t most = 1;
     for (int i = 0; i < classes; ++i) {
       const Class& k = cls[i];
       const int64_t ns = std::max<int64_t>(1, int64_t(k.last + c - 1) / c);
-      any |= ns > 1;
+      most = std::max(most, ns);
       const double over = each + (ns > 1 ? split : 0);
       const int parts = k.first < 0.75 * k.last ? 4 : 1;   // a causal prompt's tiles differ
       for (int q = 0; q < parts; ++q) {
@@ -141,7 +142,7 @@ inline int attn_chunk(const AttnWork* w, int n, int64_t kv_heads, int64_t slots,
     }
     double cost = deal.finish(slots);
     if (shared > 0) cost = std::min(cost, shared * deal.finish(2 * slots));
-    if (any) cost += join;
+    if (most > 1) cost += join + joined * double(most);
     if (c == top || cost < best_cost) {
       best = c;
       best_cost = cost;
@@ -266,13 +267,19 @@ inline void attn_plan(AttnPlan& o, const KvView& c, const KvSeqs& s, int n_heads
   const double unit_bytes = double(kv_row_bytes(c.dim, cache_dtype)) * 2 * (1 << kDecodeUnitShift);
   const int dblocks = cache_dtype == LORA_KV_E2M1 ? decode4_blocks(c.dim, o.decode_tile)
                                                   : decode_blocks(c.dim, cache_dtype == LORA_KV_E4M3 ? 1 : 2, o.decode_tile);
-  const int dchunk = attn_chunk(dec, nd, c.kv_heads, dblocks * kAttnCUs, (dblocks == 2 ? 32768 : 98304) / unit_bytes,
-                                o.decode_rows * c.dim * 8 / unit_bytes, 98304 / unit_bytes, 2, 0);
+  // Over e2m1 pages a unit is a quarter as long, so that starts and joins count for more of them: with the bytes above,
+  // one stream of 8,019 positions, 8 heads of 128, was cut into 125 items a head and took 29 us, with these 13.5; six
+  // chats of 256-wide heads 31 both ways, 64 streams 140.
+  const int64_t dslots = dblocks * kAttnCUs;
+  const int dchunk = cache_dtype == LORA_KV_E2M1
+                         ? attn_chunk(dec, nd, c.kv_heads, dslots, 12, 1, 6, 0.2, 2, 0)
+                         : attn_chunk(dec, nd, c.kv_heads, dslots, (dblocks == 2 ? 32768 : 98304) / unit_bytes,
+                                      o.decode_rows * c.dim * 8 / unit_bytes, 98304 / unit_bytes, 0, 2, 0);
   attn_fill(o.decode, dec, nd, dchunk, s, c.kv_heads, o.decode_tile, group);
   // In units of 64 positions against 256 rows; a split item's sums are 256 fp32 rows written and read, and the
   // join's launch counts for more of the shorter units of narrow heads.
   const int pchunk = prompt_items >= 16 * kAttnCUs ? 1 << 30
-                                                   : attn_chunk(pro, np, c.kv_heads, kAttnCUs, 1.5, 2.5, 768.0 / c.dim, 4,
+                                                   : attn_chunk(pro, np, c.kv_heads, kAttnCUs, 1.5, 2.5, 768.0 / c.dim, 0, 4,
                                                                 c.dim == 64 ? 1.6 : 0);
   attn_fill(o.prompt, pro, np, pchunk, s, c.kv_heads, kPromptRows, group);
 

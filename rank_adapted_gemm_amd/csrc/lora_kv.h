@@ -233,9 +233,11 @@ constexpr int decode_wave_lds(int dim, int elem_bytes, int tile_rows) {
   const int out = tile_rows * (dim + 4) * 4;
   return ring > out ? ring : out;
 }
-// Over e2m1 pages: one step's values in 16 bits, and at the end the outputs.
+// Over e2m1 pages a step's values are 16 bits wide in LDS, of 256-wide heads one half after the other, and so are the
+// fp32 outputs at the end.
+constexpr int decode4_halves(int dim) { return dim == 256 ? 2 : 1; }
 constexpr int decode4_wave_lds(int dim, int tile_rows) {
-  const int step = 2 * dim << kDecodeUnitShift, out = tile_rows * (dim + 4) * 4;
+  const int width = dim / decode4_halves(dim), step = 2 * width << kDecodeUnitShift, out = tile_rows * (width + 4) * 4;
   return step > out ? step : out;
 }
 // Decode blocks that share a CU's 160 KiB.
@@ -243,7 +245,11 @@ constexpr int blocks_of_lds(int wave_lds) { return kDecodeWaves * wave_lds <= 76
 constexpr int decode_blocks(int dim, int elem_bytes, int tile_rows) {
   return blocks_of_lds(decode_wave_lds(dim, elem_bytes, tile_rows));
 }
-constexpr int decode4_blocks(int dim, int tile_rows) { return blocks_of_lds(decode4_wave_lds(dim, tile_rows)); }
+// Registers are the limit there: 125 a thread at 128-wide heads, 183 at 256-wide ones, whose three blocks would spill
+// (six chats 36 instead of 31 us).
+constexpr int decode4_blocks(int dim, int tile_rows) {
+  return tile_rows == 16 ? (dim == 256 ? 2 : 4) : (dim == 256 ? 1 : dim == 128 ? 2 : 4);
+}
 
 // Bytes of a position's keys (or values) of one head.
 constexpr int kv_row_bytes(int dim, int cache_dtype) {
