@@ -89,7 +89,8 @@ struct WeightType<__bf16, true> {
 //
 // F4: e2m1 pages.  A wave brings its 16 positions' codes to a stage of its own in LDS two steps ahead, and a step
 // ahead makes T of them in the tile, so that products, borders and hidden values are those of 16-bit pages and each
-// code is converted once a block.
+// code is converted once a block, not once a wave as e4m3 codes are.  16,002 rows of 16 heads of 256 over 4: 1.65 ms on
+// a card where 16-bit pages take as long; 8,000 rows of 32 heads of 128 500 us (16-bit 485), of 16 of 64 175 (171).
 template <typename T, bool F8, int DIM, bool F4>
 __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(AttnArgs a, AttnPart part) {
   using R = Row<F8, DIM>;
@@ -193,38 +194,50 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
                                there ? group_bytes >> 4 : 0u);
     if (somebad && !values && lane == 0) bad[it & (2 * LOOK - 1)][grp] = hi == -2;
   };
-  // e2m1: piece x of the group is 64 / BLK rows, a block a lane
+  // e2m1: piece x of the group is 64 / BLK rows, a block a lane (64-wide heads: all 16, which half of the lanes load).
+  // To convert them a lane takes a block, or half of one at 64-wide heads.
+  constexpr int WORDS = DIM == 64 ? 2 : 4, PARTS = DIM / 8 / WORDS;   // words of codes a lane; lanes of a row
   const uint32_t stage = lds0 + 4 * TILE + wave * (PIECES * 1024);
-  const int prow = lane / BLK, pblk = lane % BLK;
-  const uint32_t code_off = uint32_t(prow) * uint32_t(a.c.token_stride) + uint32_t(pblk) * 16;
-  const uint32_t exp_off = uint32_t(prow) * (uint32_t(a.c.token_stride) >> 4) + uint32_t(pblk);
+  const int prow = lane / PARTS, ppart = lane % PARTS;
+  const uint32_t code_off = uint32_t(lane / BLK) * uint32_t(a.c.token_stride) + uint32_t(lane % BLK) * 16;
+  const uint32_t exp_off = uint32_t(prow) * (uint32_t(a.c.token_stride) >> 4) + uint32_t(ppart * WORDS >> 2);
   uint32_t exps[PIECES];
   auto fetch = [&] {   // what aim() aimed at
 #pragma unroll
     for (int x = 0; x < PIECES; ++x) {
       const uint32_t rows = uint32_t(x * (64 / BLK)) * uint32_t(a.c.token_stride);
-      const bool there = 16 * BLK >= 64 || lane < 16 * BLK;   // 64-wide heads: half of a piece
-      dma16(rs, there ? code_off + rows : kDmaMaskedOffset, stage + x * 1024);
-      exps[x] = __builtin_amdgcn_raw_buffer_load_b8(rsrc_of_words(rs_exp), there ? exp_off + (rows >> 4) : 0xFFFFFFFFu, 0, 0);
+      dma16(rs, 16 * BLK >= 64 || lane < 16 * BLK ? code_off + rows : kDmaMaskedOffset, stage + x * 1024);
+      exps[x] = __builtin_amdgcn_raw_buffer_load_b8(rsrc_of_words(rs_exp), exp_off + (rows >> 4), 0, 0);
     }
   };
-  auto convert = [&](int it) {   // the fetched step's codes, to its tile
+  // The fetched step's codes leave the stage, which is filled again, and go to their tile.  A row's blocks lie 64 bytes
+  // apart, so that lanes would meet on LDS banks, two and two; half of them write their chunks in another order.
+  const int odd = DIM == 256 ? (ppart >> 2) & 1 : (DIM == 128 && values ? prow & 1 : 0);
+  auto convert = [&](int it, auto&& refill) {
+    typedef uint32_t words __attribute__((ext_vector_type(WORDS)));
     typedef __attribute__((address_space(3))) u32x4* p16;
+    typedef __attribute__((address_space(3))) words* pw;
     const uint32_t tile = lds0 + (values ? 2 * TILE : 0) + (it & 1) * TILE;
+    words w[PIECES];
+    float s[PIECES];
+#pragma unroll
+    for (int x = 0; x < PIECES; ++x) {
+      w[x] = *pw(uintptr_t(stage + x * 1024 + lane * (WORDS * 4)));
+      s[x] = scale_of(exps[x]);
+    }
+#pragma unroll
+    for (int x = 0; x < PIECES; ++x) asm volatile("" : "+v"(w[x]), "+v"(s[x]) : : "memory");   // they are in registers
+    refill();
 #pragma unroll
     for (int x = 0; x < PIECES; ++x) {
       const int r = x * (64 / BLK) + prow;
-      const u32x4 w = *p16(uintptr_t(stage + x * 1024 + lane * 16));
-      const float s = scale_of(exps[x]);
       const uint32_t row = tile + uint32_t(grp * 16 + r) * R::kBytes;
-      const uint32_t sw = uint32_t(pblk * 4) ^ uint32_t(values ? V::swizzle(r) : R::key_swizzle(r));
-      if (16 * BLK >= 64 || lane < 16 * BLK) {
+      const uint32_t sw = uint32_t(ppart * WORDS + odd) ^ uint32_t(values ? V::swizzle(r) : R::key_swizzle(r));
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          *p16(uintptr_t(row + ((sw ^ uint32_t(k)) << 4))) = __builtin_bit_cast(u32x4, from_e2m1<T>(w[k], s));
-      }
+      for (int k = 0; k < WORDS; ++k)
+        *p16(uintptr_t(row + ((sw ^ uint32_t(k)) << 4))) =
+            __builtin_bit_cast(u32x4, from_e2m1<T>(odd ? w[x][k ^ 1] : w[x][k], s[x]));
     }
-    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");   // the stage may be filled again
   };
   auto load = [&](int it, int x) {   // one of the group's R::kLoads
     if constexpr (F4) return;
@@ -341,9 +354,10 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
   if constexpr (F4) {
     fetch();
     asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
-    convert(0);
-    aim(1);
-    fetch();
+    convert(0, [&] {
+      aim(1);
+      fetch();
+    });
   }
 #pragma unroll
   for (int x = 0; x < R::kLoads; ++x) load(0, x);
@@ -366,16 +380,16 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
 #pragma unroll
         for (int x = EARLY * n / of; x < EARLY * (n + 1) / of; ++x) load(it + 1, x);
       });
-      if constexpr (F4) {
-        convert(it + 1);
-        fetch();
-      }
       weights(st, w);
       outputs(vt, w, [&](int n, int of) {
 #pragma unroll
         for (int x = LATE * n / of; x < LATE * (n + 1) / of; ++x) load(it + 1, EARLY + x);
       });
+      // Between the halves, or amid the second, where its exponentials follow: 16,002 rows of 256-wide heads 1,666
+      // and 1,654 us, 8,000 of 128 498 and 505 (amid the first: 1,682, 520).
+      if constexpr (F4 && DIM == 128) convert(it + 1, fetch);
       scores(kt + 32 * R::kBytes, st, [](int, int) {});
+      if constexpr (F4 && DIM != 128) convert(it + 1, fetch);
       weights(st, w);
       outputs(vt + 32 * R::kBytes, w, [](int, int) {});
     }
@@ -390,10 +404,7 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
     }
     if (((it + LOOK) & 63) == 0) load_pages(it + LOOK);
     aim(it + LOOK);
-    if constexpr (F4) {
-      convert(it + 1);
-      fetch();
-    }
+    if constexpr (F4) convert(it + 1, fetch);
 #pragma unroll
     for (int x = 0; x < R::kLoads; ++x) load(it + 1, x);
     // A position that a row does not see may hold anything there, and its weight 0 must not meet an
