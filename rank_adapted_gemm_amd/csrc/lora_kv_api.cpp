@@ -210,7 +210,7 @@ lora_status lora_kv_append_rope(const lora_kv_cache* cache, const lora_kv_batch*
   if (!rope || rope->n_axes < 1) return LORA_EINVAL;
   if (rope->dim < 16 || rope->dim % 16 != 0 || rope->dim > a.c.dim || rope->n_axes > lora::kRopeMaxAxes)
     return LORA_EUNSUPPORTED;
-  if (!(std::fabs(rope->factor) <= 3.4e38f)) return LORA_EINVAL;   // NaN too
+  if (!std::isfinite(rope->factor)) return LORA_EINVAL;
   for (int j = 0; j < rope->dim / 2 && rope->axis; ++j) {
     if (rope->axis[j] >= rope->n_axes) return LORA_EINVAL;
     r.axis[j >> 4] |= uint32_t(rope->axis[j]) << (2 * (j & 15));

@@ -10,9 +10,10 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 constexpr int kMaxFreqs = 128;    // of a row: half of the widest head
 constexpr int kDepth = 2;         // pieces a thread has under way
 // A block takes one row, so that few rows meet many CUs (64 rows of 48 heads of 128: 5.6 us, 8.0 with two rows a block, 13
-// with four).  Many rows to e2m1 pages go two a block (8,019 rows of 48 heads: 42 against 48 us); to 16 bits that is even
-// (16,002 rows of 24 heads of 256: 82 and 82 us).
-constexpr int kManyRows = 2048;
+// with four; 3,140 rows of 48 heads of 64: 10.7 and 11.2).  Many rows to e2m1 pages go two a block (8,019 rows of 48
+// heads: 42 against 48 us), to other pages where it is even (16,002 rows of 24 heads of 256: 82 and 82 us): a grid holds
+// less than 2^32 threads.
+constexpr int kManyRows = 8192, kManyRowsE2m1 = 2048;
 constexpr int kKey = 1 << 16, kValue = 1 << 17;
 
 // Sine and cosine of t / 2^32 turns.  The quarter is taken off exactly; what is left, within an eighth of a turn either
@@ -216,7 +217,7 @@ void run_rows(const AppendArgs& a, const RopeArgs& r, int cache_dtype, hipStream
 
 template <typename T>
 void run(const AppendArgs& a, const RopeArgs& r, int cache_dtype, hipStream_t stream) {
-  if (cache_dtype == LORA_KV_E2M1 && a.rows > kManyRows) run_rows<T, 2>(a, r, cache_dtype, stream);
+  if (a.rows > (cache_dtype == LORA_KV_E2M1 ? kManyRowsE2m1 : kManyRows)) run_rows<T, 2>(a, r, cache_dtype, stream);
   else run_rows<T, 1>(a, r, cache_dtype, stream);
 }
 

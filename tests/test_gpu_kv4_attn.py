@@ -181,6 +181,23 @@ def test_large_scores(rows):
         check_out(ra.attn(c, b, p.q, scale), p.reference(scale), "bf16", 64)
 
 
+@pytest.mark.parametrize("dtype,low,high", [("f16", 127 - 20, 127 + 12), ("bf16", 127 - 100, 127 + 100)])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_small_and_large_blocks(rows, dtype, low, high):
+    """Keys' and values' exponents over the type's range, fp16's subnormal values among them."""
+    p = Problem4(23, [rows], [rows + 300], 4, 2, 128, 16, dtype)
+    used = p.ke != 255
+    for exps in (p.ke, p.ve):
+        for e in (low, high):
+            keep = exps.clone()
+            exps[used] = e
+            c, b = p.make()
+            # scores of about the usual size; outputs within the type
+            scale = 128 ** -0.5 * (2.0 ** (127 - e) if exps is p.ke else 1.0)
+            check_out(ra.attn(c, b, p.q, scale), p.reference(scale), dtype, 128)
+            exps.copy_(keep)
+
+
 @pytest.mark.parametrize("mass", [False, True])
 @pytest.mark.parametrize("rows,lens", [([1] * 150, [3000] * 20 + [1 + 7 * i % 60 for i in range(130)]),
                                        ([33 + i % 3 for i in range(140)], [1500 + 9 * i for i in range(140)])])

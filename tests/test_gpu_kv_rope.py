@@ -170,6 +170,38 @@ def test_rotation_of_a_difference_is_that_of_positions():
     assert max(dots) - min(dots) <= 2 * (2 * 2.0 ** -11 + 4 * TURN) * size
 
 
+@pytest.mark.parametrize("cache", ["same", "e2m1"])
+def test_the_most_rows(cache):
+    """2^24 rows of one sequence, the last among them checked."""
+    n, dim, page = 1 << 24, 64, 4096
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(n, 2, dim, generator=g, device="cuda", dtype=torch.float16)
+    if cache == "e2m1":
+        pool = [torch.zeros(n // page, page, 1, dim // w, dtype=torch.uint8, device="cuda") for w in (2, 2, 32, 32)]
+    else:
+        pool = [torch.zeros(n // page, page, 1, dim, dtype=torch.float16, device="cuda") for _ in range(2)]
+    table = torch.arange(n // page, dtype=torch.int32, device="cuda")[None]
+    c, b, rope = ra.KVCache(*pool), ra.KVBatch([0, n], [n], table), ra.Rope(dim)
+    q = ra.kv_append(c, b, x[:, :1], x[:, 1:], rope, q=x[:, 1:])
+    rows = np.r_[0:3, 8191:8194, n // 2 - 1:n // 2 + 1, n - 5:n]
+    at = np.array([rows])
+    for got, src in ((q, x[:, 1:]), (pool[0], x[:, :1])):
+        want = blocks_ref.rotate(values(src[rows]), at, rope.freqs)
+        fp32 = TURN * blocks_ref.partners(values(src[rows]), dim // 2)
+        if got is pool[0] and cache == "e2m1":
+            flat = [t.flatten(0, 1)[rows].cpu().numpy() for t in (pool[0], pool[2])]
+            check_codes(*flat, want, fp32, "f16")
+        else:
+            assert near(values(got.flatten(0, 1)[rows] if got is pool[0] else got[rows]), want, fp32, "f16")
+    v = values(x[rows][:, 1:])
+    if cache == "e2m1":
+        codes, exps = blocks_ref.quantize(v, "f16")
+        np.testing.assert_array_equal(pool[1].flatten(0, 1)[rows].cpu().numpy(), codes)
+        np.testing.assert_array_equal(pool[3].flatten(0, 1)[rows].cpu().numpy(), exps)
+    else:
+        np.testing.assert_array_equal(values(pool[1].flatten(0, 1)[rows]), v)
+
+
 @pytest.mark.parametrize("cache", ["same", "e4m3", "e2m1"])
 def test_without_queries_and_with_views(cache):
     p = problem(7, [30, 2], [30, 90], 4, 2, 64, 32, "bf16", cache, q_gap=8)
