@@ -136,6 +136,95 @@ def test_every_row_that_sees_a_value_gets_it(rows, length, window, sinks, back, 
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("exp", [255, "infinite"])
+@pytest.mark.parametrize("rows,length,window,sinks,back", [
+    (1, 200, -1, 0, 0), (1, 4000, -1, 0, 70), (3, 90, -1, 0, 1), (50, 180, -1, 0, 20), (40, 700, -1, 0, 300), (60, 200, 30, 0, 33),
+    (1, 200, 40, 3, 60)])
+def test_keys_that_are_not_numbers(rows, length, window, sinks, back, exp, dtype):
+    """Rows that see a NaN key are NaN, with their weights; the others are as without it."""
+    p = Problem4(5, [rows], [length], 4, 2, 128, 16, dtype)
+    pos = length - rows - back
+    ref = p.reference(window=window, sinks=sinks)
+    p.ke[int(p.table[0, pos // 16]), pos % 16, 0, 2] = 255 if exp == 255 else 254
+    p.k[int(p.table[0, pos // 16]), pos % 16, 0, 32:48] = 0x7F if exp == 255 else 0xF7   # 6 and -6: inf - inf
+    c, b = p.make()
+    mass = torch.zeros(1, 2, length, device="cuda")
+    t = length - rows + np.arange(rows)
+    sees = (t >= pos) & ((window < 0) | (pos > t - window) | (pos < sinks))
+    for m in (None, mass):
+        y = values(ra.attn(c, b, p.q, window=window, sinks=sinks, mass_out=m))
+        hit = np.zeros(y.shape, dtype=bool)
+        hit[sees, :2] = True
+        if exp == 255:
+            assert np.isnan(y[hit]).all()
+        y[hit] = ref["out"][hit]         # an infinite key: whatever a row that sees it gets
+        check_out(torch.from_numpy(y), ref, dtype, 128)
+    got, want = values(mass)[0], ref["mass"][0]
+    same = np.ones(got.shape, dtype=bool)
+    for j in np.flatnonzero(sees):
+        q = np.arange(length)
+        seen = (q <= t[j]) & ((window < 0) | (q > t[j] - window) | (q < sinks))
+        same[0, seen] = False
+        if exp == 255:
+            assert np.isnan(got[0, seen]).all()
+    tol = (float(np.max(weight_error(ref, 128))) + (2 * rows + 2) * 2.0 ** -24) * want
+    assert (np.abs(got - want) <= tol)[same].all()
+
+
+@pytest.mark.parametrize("rows,lens", [([1, 1, 1], [500, 90, 40]), ([4, 2, 3], [300, 104, 99]), ([33, 80, 5], [200, 120, 70])])
+def test_weights_of_rows_that_need_an_invalid_page(rows, lens):
+    """NaN at the positions that those rows see; every other position's weight as without it."""
+    window, sinks, page, heads, dim = 20, 3, 16, 4, 128
+    p = Problem4(9, rows, lens, heads, 2, dim, page)
+    ref = p.reference(window=window, sinks=sinks)
+    bad = lens[1] // page - 1                      # the last whole page of the second sequence
+    p.table[1, bad] = -3
+    c, b = p.make()
+    out = torch.zeros(3, 2, max(lens), device="cuda")
+    y = values(ra.attn(c, b, p.q, window=window, sinks=sinks, mass_out=out))
+    got = values(out)
+    rel = float(np.max(weight_error(ref, dim))) + (max(rows) * 2 + 2) * 2.0 ** -24
+    for i, n in enumerate(lens):
+        lost = np.zeros(n, dtype=bool)
+        for j in range(rows[i]):
+            t = n - rows[i] + j
+            q = np.arange(n)
+            seen = (q <= t) & ((q > t - window) | (q < sinks))
+            if i == 1 and seen[bad * page:(bad + 1) * page].any():
+                lost |= seen
+                assert np.isnan(y[p.q_starts[i] + j]).all()
+            else:
+                assert np.isfinite(y[p.q_starts[i] + j]).all()
+        assert np.isnan(got[i, :, :n][:, lost]).all()
+        want = ref["mass"][i, :, :n]
+        assert (np.abs(got[i, :, :n] - want) <= rel * want)[:, ~lost].all()
+
+
+@pytest.mark.parametrize("dim,heads,lens", [(128, 4, [9000, 40]), (256, 8, [7000, 900]), (64, 1, [12000, 12000])])
+def test_split_rows_in_a_graph(dim, heads, lens):
+    """Rows that their last item joins, captured, with eager calls between the replays."""
+    p = Problem4(41, [1, 1], lens, heads, 1, dim, 16)
+    c, b = p.make()
+    assert ra.attn_plan(c, b, heads)[0]["joined"] == 1
+    eager = ra.attn(c, b, p.q)
+    check_out(eager, p.reference(), "bf16", dim)
+    ws, out = ra.attn_workspace(c, b, heads), torch.empty_like(eager)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ra.attn(c, b, p.q, out=out, workspace=ws)
+        ra.attn(c, b, p.q, out=out, workspace=ws)   # the same workspace again, in order
+    for n in range(5):
+        out.fill_(7)
+        if n == 2:
+            ws.fill_(0xFF)
+        g.replay()
+        other = ra.attn(c, b, p.q)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager) and torch.equal(other, eager)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("rows,lens,window,sinks", [
     ([1, 1, 0], [700, 1, 30], -1, 0), ([1, 2], [900, 333], 100, 7), ([80, 1], [80, 300], -1, 0),
     ([150], [400], 60, 5), ([20, 35], [1500, 35], -1, 0)])

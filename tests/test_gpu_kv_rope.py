@@ -220,6 +220,57 @@ def test_invalid_pages_are_skipped_and_queries_are_not(cache):
     check_append(p, cache, "bf16", ra.Rope(64), None)
 
 
+def test_the_most_sequences():
+    rows = [(3 * i) % 4 for i in range(256)]
+    lens = [n + (7 * i) % 30 for i, n in enumerate(rows)]
+    for dtype, cache in (("bf16", "same"), ("f16", "e2m1")):
+        check_append(problem(14, rows, lens, 2, 1, 64, 16, dtype, cache), cache, dtype, ra.Rope(64), None)
+
+
+@pytest.mark.parametrize("n,cache,dtype", [(2051, "e2m1", "bf16"), (8195, "same", "f16"), (8193, "e4m3", "bf16")])
+def test_many_rows_go_as_few_do(n, cache, dtype):
+    """An odd number of rows that go two a block, bit for bit as in two calls of fewer."""
+    half = n // 2
+    p = problem(16, [half, n - half], [half + 100, n - half], 3, 1, 128, 64, dtype, cache)
+    c, b = p.make()
+    rope = ra.Rope(96, base=3e5)
+    q = ra.kv_append(c, b, p.new_k, p.new_v, rope, q=p.q)
+    one = [t.clone() for t in pools(p, cache)]
+    for t in pools(p, cache):
+        (t.view(torch.uint8) if cache == "e4m3" else t).fill_(3)
+    for i, (a, z) in enumerate(((0, half), (half, n))):
+        b = ra.KVBatch([0, z - a], [p.kv_len[i]], p.table[i:i + 1])
+        step = (z - a + 2) // 3                     # and those in three
+        for s in range(0, z - a, step):
+            e = min(z - a, s + step)
+            length = p.kv_len[i] - (z - a) + e
+            part = ra.kv_append(c, ra.KVBatch([0, e - s], [length], p.table[i:i + 1]), p.new_k[a + s:a + e], p.new_v[a + s:a + e],
+                                rope, q=p.q[a + s:a + e])
+            assert torch.equal(part, q[a + s:a + e])
+        pos = torch.arange(p.kv_len[i] - (z - a), p.kv_len[i], device="cuda")
+        for old, new in zip(one, pools(p, cache)):
+            raw_old, raw_new = (t.view(torch.uint8) if cache == "e4m3" else t for t in (old, new))
+            at = (p.table[i][pos // 64].long(), pos % 64)
+            assert torch.equal(raw_old[at], raw_new[at])
+
+
+def test_another_stream():
+    p = problem(17, [40, 1], [40, 90], 4, 2, 64, 16, "bf16", "e2m1")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    busy = torch.randn(4096, 4096, device="cuda")
+    for _ in range(4):
+        busy = busy @ busy.clamp(-1e-3, 1e-3)      # the current stream has work of its own
+    rope = ra.Rope(64)
+    c, b = p.make()
+    q = ra.kv_append(c, b, p.new_k, p.new_v, rope, q=p.q, stream=side)
+    side.synchronize()
+    want, fp32 = rotated(p.q, p, rope, None)
+    assert near(values(q), want, fp32, "bf16")
+    with pytest.raises(TypeError):
+        ra.kv_append(c, b, p.new_k, p.new_v, rope, q=p.q, stream=side.cuda_stream)
+
+
 def test_rotation_by_zero_changes_nothing():
     for dtype in ("bf16", "f16"):
         p = problem(9, [20], [20], 3, 1, 128, 16, dtype, "same")
