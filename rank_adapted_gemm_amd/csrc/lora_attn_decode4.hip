@@ -94,24 +94,34 @@ __global__ __launch_bounds__(kWaves * 64, decode4_blocks(DIM, QT * 16)) void dec
   const int vrow = lane / C::kRowLanes, vpart = lane % C::kRowLanes;
   const uint32_t kcode = uint32_t(col) * ts + uint32_t(qd) * C::kBytes, kexp = uint32_t(col) * te + uint32_t(qd * C::kBytes >> 4);
   const uint32_t vcode = uint32_t(vrow) * ts + uint32_t(vpart) * C::kBytes, vexp = uint32_t(vrow) * te + uint32_t(vpart * C::kBytes >> 4);
-  // A step's groups in one of the pools.  Nowhere: loads through a descriptor without bytes give zeros.
-  struct Aim {
-    __amdgpu_buffer_rsrc_t codes[2], exps[2];
-    uint32_t bad;
+  // Where a step's groups lie.  Nowhere: loads through a descriptor without bytes give zeros.
+  struct Place {
+    int64_t at[2];
+    uint32_t bytes[2], bad;
   };
-  auto aim = [&](int i, const char* codes, const uint8_t* exps) {
-    Aim r;
+  auto place = [&](int i) {
+    Place r;
     r.bad = 0;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const int hi = __builtin_amdgcn_readlane(place_hi[g], i & 63);
       const uint32_t lo = uint32_t(__builtin_amdgcn_readlane(place_lo[g], i & 63));
       const bool there = hi >= 0 && i < mine;
-      const int64_t at = there ? int64_t(hi) << 32 | lo : 0;
-      const uint32_t bytes = there ? group_bytes : 0u;
-      r.codes[g] = make_rsrc(codes + at, bytes);
-      r.exps[g] = make_rsrc(exps + (at >> 4), bytes >> 4);
+      r.at[g] = there ? int64_t(hi) << 32 | lo : 0;
+      r.bytes[g] = there ? group_bytes : 0u;
       r.bad |= hi == -2 ? 1u << g : 0u;
+    }
+    return r;
+  };
+  struct Aim {
+    __amdgpu_buffer_rsrc_t codes[2], exps[2];
+  };
+  auto aim = [&](const Place& p, const char* codes, const uint8_t* exps) {
+    Aim r;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      r.codes[g] = make_rsrc(codes + p.at[g], p.bytes[g]);
+      r.exps[g] = make_rsrc(exps + (p.at[g] >> 4), p.bytes[g] >> 4);
     }
     return r;
   };
@@ -152,8 +162,9 @@ __global__ __launch_bounds__(kWaves * 64, decode4_blocks(DIM, QT * 16)) void dec
   load_pages(0);
   // Codes are refilled once they were used, so that each run has about a step to arrive.
   {
-    const Aim ka = aim(0, a.c.k, a.c.k_exp), va = aim(0, a.c.v, a.c.v_exp);
-    badk = ka.bad;
+    const Place start = place(0);
+    const Aim ka = aim(start, a.c.k, a.c.k_exp), va = aim(start, a.c.v, a.c.v_exp);
+    badk = start.bad;
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) fill(ka, h, kcode, kexp, kc[h], ke[h]);
     __builtin_amdgcn_sched_barrier(0);
@@ -192,10 +203,11 @@ __global__ __launch_bounds__(kWaves * 64, decode4_blocks(DIM, QT * 16)) void dec
     const int p0 = units.unit(u0 + wave + i * kWaves) * kStep;
     const uint32_t badp = badk;
     if (((i + 1) & 63) == 0) load_pages(i + 1);
+    const Place after = place(i + 1);
+    badk = after.bad;
     f32x4 st[QT][2];
     {
-      const Aim next = aim(i + 1, a.c.k, a.c.k_exp);
-      badk = next.bad;
+      const Aim next = aim(after, a.c.k, a.c.k_exp);
 #pragma unroll
       for (int h = 0; h < HALVES; ++h) {
 #pragma unroll
@@ -265,8 +277,8 @@ __global__ __launch_bounds__(kWaves * 64, decode4_blocks(DIM, QT * 16)) void dec
         f32x4 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          v[e] = st[x][g][e] * c;
-          const float wt = __builtin_amdgcn_exp2f(v[e] - top[x]);
+          if constexpr (MASS) v[e] = st[x][g][e] * c;
+          const float wt = __builtin_amdgcn_exp2f(MASS ? v[e] - top[x] : __builtin_fmaf(st[x][g][e], c, -top[x]));
           sum[x] += wt;
           st[x][g][e] = wt;
         }
@@ -287,7 +299,7 @@ __global__ __launch_bounds__(kWaves * 64, decode4_blocks(DIM, QT * 16)) void dec
     // values: T in the wave's tile, a lane's block after the other's, then read in columns.  A wave's LDS accesses
     // are done in order.
     typedef __attribute__((address_space(3))) u32x4* p16;
-    const Aim next = aim(i + 1, a.c.v, a.c.v_exp);
+    const Aim next = aim(after, a.c.v, a.c.v_exp);
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) {
 #pragma unroll
