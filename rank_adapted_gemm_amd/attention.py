@@ -102,7 +102,8 @@ class Rope:
         Rope(128, axis=[0] * 16 + [1] * 24 + [2] * 24)      # in runs
         Rope(128, axis=[j % 3 for j in range(64)])          # in turns
 
-    ``factor`` multiplies what is rotated.  One Rope serves every layer of a GPU."""
+    ``factor`` multiplies what is rotated.  One Rope serves every layer and stream of a GPU; a captured graph needs it
+    for as long as it is replayed."""
 
     def __init__(self, dim, base=10000.0, freqs=None, axis=None, interleaved=False, factor=1.0, device=None):
         import torch
@@ -124,11 +125,17 @@ class Rope:
         device = torch.device("cuda" if device is None else device)
         self._turns = torch.frombuffer(turns, dtype=torch.int64).to(device)
         self._index = self._turns.get_device()
+        self._home = torch._C._cuda_getCurrentRawStream(self._index) if self._index >= 0 else 0
         self._axis = (ctypes.c_uint8 * half)(*axis)
 
         self._c = _bd.RopeStruct(self._turns.data_ptr(), ctypes.cast(self._axis, ctypes.c_void_p), None, 0, self.axes,
                                  self.dim, int(self.interleaved), self.factor)
         self._ref = ctypes.byref(self._c)
+
+    def _used_on(self, stream):
+        """Keeps the frequencies' memory from reuse while `stream` (None: the current one) reads them."""
+        import torch
+        self._turns.record_stream(torch.cuda.current_stream(self._index) if stream is None else stream)
 
     def _at(self, positions, rows):
         """The library's rotation with these positions."""
@@ -265,6 +272,8 @@ def kv_append(cache, batch, k, v, rope=None, positions=None, q=None, q_out=None,
         raise ValueError(f"the Rope is on GPU {rope._index}, the cache on {cache.device}")
     turn = rope._ref if positions is None else rope._at(positions, batch.rows)
     s = _handle(stream, cache)
+    if s != rope._home:
+        rope._used_on(stream)
     if q is None:
         if q_out is not None:
             raise ValueError("q_out goes with q")

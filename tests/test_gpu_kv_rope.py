@@ -269,6 +269,10 @@ def test_another_stream():
     assert near(values(q), want, fp32, "bf16")
     with pytest.raises(TypeError):
         ra.kv_append(c, b, p.new_k, p.new_v, rope, q=p.q, stream=side.cuda_stream)
+    with torch.cuda.stream(side):                  # as the current stream
+        z = ra.kv_append(c, b, p.new_k, p.new_v, rope, q=p.q)
+    side.synchronize()
+    assert torch.equal(z, q)
 
 
 def test_rotation_by_zero_changes_nothing():

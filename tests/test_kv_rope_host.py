@@ -208,6 +208,18 @@ def test_rotations_arguments_go_with_a_rotation(setup):
     assert not lib.calls
 
 
+def test_frequencies_outlive_the_calls_of_other_streams(setup, monkeypatch):
+    lib, c, b, turning, rows = setup
+    noted = []
+    monkeypatch.setattr(turning, "_used_on", lambda stream: noted.append(stream))
+    at.kv_append(c, b, rows[:, :2], rows[:, 2:], turning)
+    assert noted == []                                   # the stream that they were made on
+    monkeypatch.setattr(at, "_handle", lambda stream, cache: 7)
+    at.kv_append(c, b, rows[:, :2], rows[:, 2:], turning, stream="side")
+    at.kv_append(c, b, rows[:, :2], rows[:, 2:], turning, q=rows)
+    assert noted == ["side", None]
+
+
 def test_caches_in_4_bits_refuse_wrong_exponents(monkeypatch):
     monkeypatch.setattr(bd, "_check_operands", lambda *a: None)
     k = torch.zeros(4, 16, 2, 64, dtype=torch.uint8)
