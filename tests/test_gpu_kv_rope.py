@@ -349,7 +349,8 @@ def test_other_views_of_the_pools():
 @pytest.mark.parametrize("lens,kv,dim,page,budget,sinks,recent,head_major", [
     ([1], 1, 64, 16, 1, 0, 0, True), ([0, 16, 17, 40], 2, 128, 16, 16, 3, 5, False),
     ([1300, 1023, 1024, 1025, 5], 3, 64, 48, 1000, 4, 100, True), ([3000], 1, 256, 32, 64, 0, 64, False),
-    ([500], 2, 64, 16, 100, 0, 0, True)])
+    ([500], 2, 64, 16, 100, 0, 0, True), ([2100, 700, 3], 3, 128, 48, 1300, 4, 100, False),
+    ([640, 511], 9, 64, 16, 512, 0, 7, False)])
 def test_evict(lens, kv, dim, page, budget, sinks, recent, head_major):
     need = [(min(n, budget) + page - 1) // page for n in lens]
     p = Problem4(5, [0] * len(lens), lens, kv, kv, dim, page, head_major=head_major, extra_pages=sum(need) + 1)
@@ -373,6 +374,7 @@ def test_evict(lens, kv, dim, page, budget, sinks, recent, head_major):
             for w in filled:
                 for s, pos in enumerate(want):
                     w[dst[i, s // page], s % page, h] = w[table[i, pos // page], pos % page, h]
+            np.testing.assert_array_equal(mout[i, h, :len(want)].cpu().numpy(), m[i, h, want])
     for got, w in zip(after, filled):
         np.testing.assert_array_equal(got, w)
 
