@@ -58,10 +58,9 @@
  * exponents lie in a pool of their own that has the codes' order: a row's start at a
  * sixteenth of the codes' byte offset, so the two pools are (pages, slots, heads,
  * head_dim / 2) and (pages, slots, heads, head_dim / 32) bytes in the same order of
- * dimensions.  Heads outside slots keep 16 slots of a head together, which is what a
- * block reads (64 decoding streams, 8 heads of 128, the other way: a cache line holds two
- * heads).  Values meet queries and weights in the queries' type, which holds them exactly
- * but for fp16 past 65504 (infinite there) and below 2^-24 (rounded).
+ * dimensions.  Heads outside slots read fastest: 16 slots of a head, which is what a block
+ * takes, lie together.  Values meet queries and weights in the queries' type, which holds
+ * them exactly but for fp16 past 65504 (infinite there) and below 2^-24 (rounded).
  *
  * Limits (LORA_EUNSUPPORTED beyond): head_dim 64, 128 or 256; page_size a
  * multiple of 16 up to 65536; n_seq <= LORA_MAX_SEGMENTS; kv_len <= 2^24;
@@ -127,10 +126,11 @@ typedef struct lora_kv_batch {
  *
  * E4M3 stores round-to-nearest-even(clamp(x / scale, -448, 448)), NaN as NaN.
  *
- * E2M1 gives a block the smallest power of two that leaves no value further than half a step from
- * a code's: with a = max |x| of the block, E - 127 = floor(log2 a) - 2, one more where
- * a > 7 * 2^(floor(log2 a) - 2), within -127 and 125 (bf16 rows) or 13 (fp16 rows); codes are x / 2^(E - 127) rounded to nearest,
- * ties to even, values past 6 (infinities among them) held at 6.  A block with a NaN gets E 255.
+ * E2M1 gives a block the smallest power of two that leaves no value further than half a step from a
+ * code's: with a = max |x| of the block and e = floor(log2 a) - 2, E - 127 is e, or e + 1 where
+ * a > 7 * 2^e, within -127 (also where a is 0) and 125 (bf16 rows) or 13 (fp16 rows).  Codes are
+ * x / 2^(E - 127) rounded to nearest, ties to even, magnitudes past 6 (infinities among them) held
+ * there.  A block with a NaN gets E 255.
  *
  * k and v must not overlap the cache (LORA_EINVAL).
  */

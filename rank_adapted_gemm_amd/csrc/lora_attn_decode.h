@@ -54,12 +54,12 @@ struct ValueReader16 {
 // marks go past the XCD's L2 (device scope): the other items run on other XCDs.
 
 // Whether this item found them all; `arrived`: of the row's first split, the others a head count apart.
-__device__ __forceinline__ bool all_arrived(const AttnArgs& a, const AttnSeq& sq, const uint64_t* arrived) {
+__device__ __forceinline__ bool all_arrived(const AttnArgs& a, const AttnSeq& sq, int item, const uint64_t* arrived) {
   const int tid = threadIdx.x;
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
   __syncthreads();                                // every thread's sums are where the others will look
   if (tid == 0)
-    __hip_atomic_exchange(a.arrived + blockIdx.x, a.call, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_exchange(a.arrived + item, a.call, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
   __syncthreads();
   bool missing = false;
@@ -74,12 +74,12 @@ __device__ __forceinline__ void clear_arrived(const AttnArgs& a, const AttnSeq& 
 }
 
 template <typename T, int DIM>
-__device__ __forceinline__ void join_last(const AttnArgs& a, const AttnSeq& sq, int first, int head, int tile_rows, int M,
+__device__ __forceinline__ void join_last(const AttnArgs& a, const AttnSeq& sq, int first, int item, int head, int tile_rows, int M,
                                           float vs, float* lds) {
   const int tid = threadIdx.x;
   uint64_t* arrived = a.arrived + first + head;   // of the row's first split; the others a head count apart
   const int64_t slot0 = (int64_t(first) + head) * tile_rows, step = int64_t(a.c.kv_heads) * tile_rows;
-  if (!all_arrived(a, sq, arrived)) return;
+  if (!all_arrived(a, sq, item, arrived)) return;
   const uint32_t span = uint32_t((sq.nsplit - 1) * step + tile_rows);
   const auto po = make_rsrc(a.part_o + slot0 * DIM, span * DIM * 4), pm = make_rsrc(a.part_ml + slot0 * 2, span * 8);
   // maxima and sums of all rows and splits
@@ -131,13 +131,13 @@ __device__ __forceinline__ void store_joined(const AttnArgs& a, const AttnSeq& s
 // The same for many short items: a row's factors once, by sixteen lanes, eight or sixteen of its sums under way a thread, and
 // where there are threads to spare several share a row's splits, whose parts meet in LDS.
 template <typename T, int DIM>
-__device__ __forceinline__ void join_many(const AttnArgs& a, const AttnSeq& sq, int first, int head, int tile_rows, int M,
+__device__ __forceinline__ void join_many(const AttnArgs& a, const AttnSeq& sq, int first, int item, int head, int tile_rows, int M,
                                           float* lds) {
   constexpr int DEPTH = DIM == 256 ? 16 : 8;
   const int tid = threadIdx.x, ns = sq.nsplit;
   uint64_t* arrived = a.arrived + first + head;
   const int64_t slot0 = (int64_t(first) + head) * tile_rows, step = int64_t(a.c.kv_heads) * tile_rows;
-  if (!all_arrived(a, sq, arrived)) return;
+  if (!all_arrived(a, sq, item, arrived)) return;
   const uint32_t span = uint32_t((ns - 1) * step + tile_rows);
   const auto po = make_rsrc(a.part_o + slot0 * DIM, span * DIM * 4), pm = make_rsrc(a.part_ml + slot0 * 2, span * 8);
   // each row's sum; its splits' maxima, then their factors; their sums, then parts of outputs
@@ -200,7 +200,7 @@ __device__ __forceinline__ void join_many(const AttnArgs& a, const AttnSeq& sq, 
 // The waves' rows meet in LDS, WAVE_LDS bytes a wave, in RUNS runs of their columns, and leave for the output, or where they
 // were split for the workspace.
 template <typename T, int DIM, int QT, bool MASS, int WAVE_LDS, int RUNS = 1, bool MANY = false>
-__device__ __forceinline__ void meet_waves(const AttnArgs& a, const AttnSeq& sq, int first, int head, int M, float vs, char* lds,
+__device__ __forceinline__ void meet_waves(const AttnArgs& a, const AttnSeq& sq, int first, int item, int head, int M, float vs, char* lds,
                                            float (&ml)[kDecodeWaves][QT * 16][2], const f32x4 (&o)[QT][DIM / 16],
                                            const float (&top)[QT], const float (&total)[QT]) {
   constexpr int BM = QT * 16, W = DIM / RUNS, DB = W / 16;
@@ -208,8 +208,8 @@ __device__ __forceinline__ void meet_waves(const AttnArgs& a, const AttnSeq& sq,
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int qd = lane >> 4, col = lane & 15;
   float* mo = reinterpret_cast<float*>(lds + wave * WAVE_LDS);
-  const auto po = make_rsrc(a.part_o + int64_t(blockIdx.x) * BM * DIM, BM * DIM * 4);
-  const auto pm = make_rsrc(a.part_ml + int64_t(blockIdx.x) * BM * 2, BM * 8);
+  const auto po = make_rsrc(a.part_o + int64_t(item) * BM * DIM, BM * DIM * 4);
+  const auto pm = make_rsrc(a.part_ml + int64_t(item) * BM * 2, BM * 8);
 #pragma unroll
   for (int run = 0; run < RUNS; ++run) {
     if (run > 0) __syncthreads();
@@ -251,14 +251,14 @@ __device__ __forceinline__ void meet_waves(const AttnArgs& a, const AttnSeq& sq,
         *reinterpret_cast<u32x2*>(a.out + (row * DIM + to) * 2) =
             u32x2{pack_pair<T>(acc[0] * inv, acc[1] * inv), pack_pair<T>(acc[2] * inv, acc[3] * inv)};
         // accumulated weights are taken against these, also where the rows were not split
-        if (MASS && to == 0) *reinterpret_cast<f32x2*>(a.part_ml + (int64_t(blockIdx.x) * BM + m) * 2) = f32x2{best, total};
+        if (MASS && to == 0) *reinterpret_cast<f32x2*>(a.part_ml + (int64_t(item) * BM + m) * 2) = f32x2{best, total};
       }
     }
   }
   if constexpr (!MASS) {
     if (!a.arrived || sq.nsplit == 1) return;
-    if constexpr (MANY) join_many<T, DIM>(a, sq, first, head, BM, M, reinterpret_cast<float*>(lds));
-    else join_last<T, DIM>(a, sq, first, head, BM, M, vs, reinterpret_cast<float*>(lds));
+    if constexpr (MANY) join_many<T, DIM>(a, sq, first, item, head, BM, M, reinterpret_cast<float*>(lds));
+    else join_last<T, DIM>(a, sq, first, item, head, BM, M, vs, reinterpret_cast<float*>(lds));
   }
 }
 

@@ -286,11 +286,11 @@ __global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16
     if constexpr (!MASS) {
       __threadfence();   // rows of slow_row lie in this XCD's L2
       if (a.arrived && sq.nsplit > 1)
-        join_last<T, DIM>(a, sq, first, item.head, BM, M, F8 ? a.c.v_scale[item.head] : 1.0f, reinterpret_cast<float*>(lds));
+        join_last<T, DIM>(a, sq, first, int(blockIdx.x), item.head, BM, M, F8 ? a.c.v_scale[item.head] : 1.0f, reinterpret_cast<float*>(lds));
     }
     return;
   }
-  meet_waves<T, DIM, QT, MASS, WAVE_LDS>(a, sq, first, item.head, M, F8 ? a.c.v_scale[item.head] : 1.0f, lds, ml, o, top, total);
+  meet_waves<T, DIM, QT, MASS, WAVE_LDS>(a, sq, first, int(blockIdx.x), item.head, M, F8 ? a.c.v_scale[item.head] : 1.0f, lds, ml, o, top, total);
 }
 
 // ---------------------------------------------------------------- join

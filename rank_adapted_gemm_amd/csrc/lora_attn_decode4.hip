@@ -39,6 +39,15 @@ __device__ __forceinline__ typename C::words load_codes(__amdgpu_buffer_rsrc_t r
   else return __builtin_bit_cast(typename C::words, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
 }
 
+// The item of a block where heads lie inside slots, so that several share a line of 128 bytes: eight neighbouring heads'
+// on one XCD (blocks go round the eight), at about one time.  64 streams of 128-wide heads 177 us, 247 in order; 16 of
+// 64-wide ones 64 and 91.  256-wide heads fill lines and stay in order (six chats 33.5 us, 34.0 otherwise), as do heads
+// outside slots (64 streams 142).
+__device__ __forceinline__ int block_near(int b, int items) {
+  const int g = b & ~63, r = b & 63;
+  return g + 64 <= items ? g + (r & 7) * 8 + (r >> 3) : b;
+}
+
 // QT: 16-row columns of packed rows.  MASS: scores go to the workspace.
 template <typename T, int DIM, int QT, bool MASS>
 __global__ __launch_bounds__(kWaves * 64, decode4_blocks(DIM, QT * 16)) void decode4_kernel(AttnArgs a, AttnPart part) {
@@ -56,11 +65,13 @@ __global__ __launch_bounds__(kWaves * 64, decode4_blocks(DIM, QT * 16)) void dec
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int qd = lane >> 4, col = lane & 15;
-  const int s = seq_of_item(part, blockIdx.x);
+  const bool near = DIM < 256 && a.c.head_stride < a.c.token_stride;
+  const int b = near ? block_near(blockIdx.x, part.items) : int(blockIdx.x);
+  const int s = seq_of_item(part, b);
   const AttnSeq sq = part.seq[s];
   const int first = s == 0 ? 0 : part.seq[s - 1].item_end;
   const int M = sq.rows * a.group;
-  const AttnItem item = attn_item(int(blockIdx.x) - first, a.c.kv_heads, sq.nsplit, 1);
+  const AttnItem item = attn_item(b - first, a.c.kv_heads, sq.nsplit, 1);
   const int t0 = sq.kv_len - sq.rows, t_lo = t0, t_hi = sq.kv_len - 1;
   const Units units = units_of(t_lo, t_hi, a.window, a.sinks, kDecodeUnitShift);
   const int u0 = split_begin(units.count, item.split, sq.nsplit);
@@ -196,7 +207,7 @@ __global__ __launch_bounds__(kWaves * 64, decode4_blocks(DIM, QT * 16)) void dec
   float* scores = nullptr;
   const int score_row = score_steps(units, sq.nsplit) * kStep;
   if constexpr (MASS)
-    scores = a.scores + int64_t(sq.score) * kStep + ((int64_t(blockIdx.x) - first) * M + col) * score_row + qd * 4;
+    scores = a.scores + int64_t(sq.score) * kStep + (int64_t(b - first) * M + col) * score_row + qd * 4;
   bool again = false;
 
   for (int i = 0; i < mine; ++i) {
@@ -340,15 +351,15 @@ __global__ __launch_bounds__(kWaves * 64, decode4_blocks(DIM, QT * 16)) void dec
   if (__syncthreads_or(again)) {
     for (int m = wave; m < M; m += kWaves)
       slow_row<T, false, DIM, true>(a, sq, pages, units, u0, nu, kStep, t0, item.head, m,
-                                    sq.nsplit > 1 ? int64_t(blockIdx.x) * BM + m : -1,
-                                    sq.nsplit > 1 || MASS ? int64_t(blockIdx.x) * BM + m : -1);
+                                    sq.nsplit > 1 ? int64_t(b) * BM + m : -1,
+                                    sq.nsplit > 1 || MASS ? int64_t(b) * BM + m : -1);
     if constexpr (!MASS) {
       __threadfence();   // rows of slow_row lie in this XCD's L2
-      if (a.arrived && sq.nsplit > 1) join_many<T, DIM>(a, sq, first, item.head, BM, M, reinterpret_cast<float*>(lds));
+      if (a.arrived && sq.nsplit > 1) join_many<T, DIM>(a, sq, first, b, item.head, BM, M, reinterpret_cast<float*>(lds));
     }
     return;
   }
-  meet_waves<T, DIM, QT, MASS, WAVE_LDS, HALVES, true>(a, sq, first, item.head, M, 1.0f, lds, ml, o, top, total);
+  meet_waves<T, DIM, QT, MASS, WAVE_LDS, HALVES, true>(a, sq, first, b, item.head, M, 1.0f, lds, ml, o, top, total);
 }
 
 template <typename T, int DIM, int QT>

@@ -233,6 +233,10 @@ constexpr int decode_wave_lds(int dim, int elem_bytes, int tile_rows) {
   const int out = tile_rows * (dim + 4) * 4;
   return ring > out ? ring : out;
 }
+// Decode blocks that share a CU's 160 KiB.
+constexpr int decode_blocks(int dim, int elem_bytes, int tile_rows) {
+  return kDecodeWaves * decode_wave_lds(dim, elem_bytes, tile_rows) <= 76 * 1024 ? 2 : 1;
+}
 // Over e2m1 pages a step's values are 16 bits wide in LDS, of 256-wide heads one half after the other, and so are the
 // fp32 outputs at the end.
 constexpr int decode4_halves(int dim) { return dim == 256 ? 2 : 1; }
@@ -240,13 +244,8 @@ constexpr int decode4_wave_lds(int dim, int tile_rows) {
   const int width = dim / decode4_halves(dim), step = 2 * width << kDecodeUnitShift, out = tile_rows * (width + 4) * 4;
   return step > out ? step : out;
 }
-// Decode blocks that share a CU's 160 KiB.
-constexpr int blocks_of_lds(int wave_lds) { return kDecodeWaves * wave_lds <= 76 * 1024 ? 2 : 1; }
-constexpr int decode_blocks(int dim, int elem_bytes, int tile_rows) {
-  return blocks_of_lds(decode_wave_lds(dim, elem_bytes, tile_rows));
-}
-// Registers are the limit there: 125 a thread at 128-wide heads, 183 at 256-wide ones, whose three blocks would spill
-// (six chats 36 instead of 31 us).
+// Decode blocks that share a CU there.  Registers are the limit: 125 a thread at 128-wide heads, 185 at 256-wide ones,
+// which three blocks would spill (six chats 36 instead of 31 us).
 constexpr int decode4_blocks(int dim, int tile_rows) {
   return tile_rows == 16 ? (dim == 256 ? 2 : 4) : (dim == 256 ? 1 : dim == 128 ? 2 : 4);
 }

@@ -288,6 +288,25 @@ def test_small_and_large_blocks(rows, dtype, low, high):
 
 
 @pytest.mark.parametrize("mass", [False, True])
+@pytest.mark.parametrize("heads,kv,dim,rows,lens", [
+    (8, 8, 128, [1] * 9, [700 + 531 * i for i in range(9)]), (6, 3, 64, [1] * 43, [1 + 97 * i % 1200 for i in range(43)]),
+    (16, 16, 64, [1, 2, 1, 1], [3000, 40, 1, 129]), (10, 5, 128, [3] + [1] * 30, [900] + [31 * i for i in range(1, 31)])])
+def test_heads_inside_slots(heads, kv, dim, rows, lens, mass):
+    """Items in eights of neighbouring heads, and those behind the last 64."""
+    p = Problem4(71, rows, lens, heads, kv, dim, 32, head_major=False)
+    assert p.k.stride(2) < p.k.stride(1)
+    c, b = p.make()
+    plan = ra.attn_plan(c, b, heads, mass=mass)
+    assert sum(x["items"] for x in plan) >= 64
+    out = torch.zeros(len(lens), kv, max(lens), device="cuda") if mass else None
+    y = ra.attn(c, b, p.q, mass_out=out)
+    ref = p.reference()
+    check_out(y, ref, "bf16", dim)
+    if mass:
+        check_mass(values(out), None, ref, lens, dim, max(rows), weight_error)
+
+
+@pytest.mark.parametrize("mass", [False, True])
 @pytest.mark.parametrize("rows,lens", [([1] * 150, [3000] * 20 + [1 + 7 * i % 60 for i in range(130)]),
                                        ([33 + i % 3 for i in range(140)], [1500 + 9 * i for i in range(140)])])
 def test_more_sequences_than_one_launch_holds(rows, lens, mass):
