@@ -40,6 +40,14 @@ __device__ __forceinline__ float next_reference(float mx, float ref) {
   return __builtin_fmaxf(ref, next);
 }
 
+// A score times the scale, rounded.  Left to themselves compilers fuse the product with the subtraction of the reference,
+// so that a row's largest score, whose product the reference was made of, keeps that product's rounding error as its
+// exponent: up to half of the last bit of scores, which is 2^9 at 2^33, and all of the row's weights are 0 or infinite.
+__device__ __forceinline__ float product(float score, float c) {
+#pragma clang fp contract(off)
+  return score * c;
+}
+
 // First value of a row's sum: NaN where scores are, as with a scale that is NaN and a row that sees a position.
 // (Kernels take the scale's magnitude from a maximum with the smallest number, which drops a NaN.)
 __device__ __forceinline__ float nan_scale(float scale, const Units& units) {

@@ -200,7 +200,7 @@ __global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16
       float mx = __builtin_fmaxf(st[x][0][0], st[x][1][0]);
 #pragma unroll
       for (int e = 1; e < 4; ++e) mx = __builtin_fmaxf(mx, __builtin_fmaxf(st[x][0][e], st[x][1][e]));
-      mx = max_rows16(max_halves(mx)) * c;
+      mx = product(max_rows16(max_halves(mx)), c);
       if (__any(ahead<T>(mx, top[x]))) {
         const float next = next_reference<T>(mx, top[x]), keep = __builtin_amdgcn_exp2f(top[x] - next);
         top[x] = next;
@@ -214,7 +214,7 @@ __global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16
         f32x4 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          v[e] = st[x][g][e] * c;
+          v[e] = product(st[x][g][e], c);
           const float wt = __builtin_amdgcn_exp2f(v[e] - top[x]);
           sum[x] += wt;
           st[x][g][e] = wt;
