@@ -419,7 +419,8 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, AttnPart part, in
 template <typename T, int DIM>
 __global__ __launch_bounds__(256) void decode_finish_kernel(AttnArgs a, AttnPart part, int tile_rows, bool f8,
                                                             int weight_blocks) {
-  __shared__ float lse[kAttnDecodeMaxRows];
+  // a row's reference and the logarithm of its sum, apart: far from 0 their sum would lose the second
+  __shared__ f32x2 rows[kAttnDecodeMaxRows];
   const int s = blockIdx.z, head = blockIdx.y;
   const AttnSeq sq = part.seq[s];
   const int first = s == 0 ? 0 : part.seq[s - 1].item_end;
@@ -441,7 +442,7 @@ __global__ __launch_bounds__(256) void decode_finish_kernel(AttnArgs a, AttnPart
     for (int m = threadIdx.x >> 4; m < M; m += 16) {   // sixteen rows at a time
       float top, total;
       row_total<16>(a.part_ml, slot0 + m, step, sq.nsplit, top, total);
-      if ((threadIdx.x & 15) == 0) lse[m] = total == 0 ? INFINITY : top + __builtin_log2f(total);   // nothing seen: no weight
+      if ((threadIdx.x & 15) == 0) rows[m] = total == 0 ? f32x2{INFINITY, 0} : f32x2{top, __builtin_log2f(total)};   // nothing seen: no weight
     }
     __syncthreads();
     if (met) {
@@ -452,7 +453,7 @@ __global__ __launch_bounds__(256) void decode_finish_kernel(AttnArgs a, AttnPart
 #pragma unroll 4
       for (int m = 0; m < M; ++m) {
         const float x = sc[int64_t(m) * score_row];
-        sum += x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(x - lse[m]);   // -inf: not seen
+        sum += x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((x - rows[m][0]) - rows[m][1]);   // -inf: not seen
       }
     }
   }

@@ -149,3 +149,26 @@ def test_decoded_rows_of_dense_scores(dim, cache, dtype, magnitude):
 @pytest.mark.parametrize("cache", [None, "e2m1"])
 def test_decoded_rows_split_over_items(cache, dtype):
     check(problem(29, [1], [5000], 4, 1, 128, dtype, cache), 1.1 * 2.0 ** 30, most_unclear=0.05)
+
+
+@kinds
+@pytest.mark.parametrize("rows,lens,window,sinks", [([1], [310], -1, 0), ([3, 1], [700, 33], -1, 0), ([9], [300], 60, 5)])
+def test_weights_of_decoded_rows_with_ties(rows, lens, window, sinks, cache, dtype, magnitude):
+    """Positions of the same score share a row's weight, which adds up to 1."""
+    p = with_ties(magnitude, rows, lens, cache, dtype)
+    for lead in (1.3, 1.77):
+        check(p, lead * 2.0 ** (magnitude - 8), window, sinks, weights=True)
+
+
+@kinds
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_weights_of_decoded_rows_of_dense_scores(dim, cache, dtype, magnitude):
+    p, scale = dense(magnitude, [1, 2], [900, 40], dim, cache, dtype)
+    for factor in (1.0, -1.37):
+        check(p, factor * scale, most_unclear=0.05, weights=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("cache", [None, "e2m1"])
+def test_weights_of_decoded_rows_split_over_items(cache, dtype):
+    check(problem(29, [1], [5000], 4, 1, 128, dtype, cache), 1.1 * 2.0 ** 30, most_unclear=0.05, weights=True)
