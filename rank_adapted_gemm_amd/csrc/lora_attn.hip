@@ -108,6 +108,7 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
   static_assert(BM == kPromptRows, "one tile height for the host's plan");
   __shared__ __attribute__((aligned(1024))) char lds[4 * TILE + STAGE];   // keys, keys, values, values; codes
   __shared__ __attribute__((aligned(16))) int32_t bad[2 * LOOK][4];       // invalid 16-slot groups of a step
+  __shared__ float far_top[BM];                                   // references of rows far from 0
   __shared__ int32_t hit[2];                                      // steps (from 1) whose values held an infinity or NaN
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -248,7 +249,7 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
   };
 
   f32x16 o[DB];
-  float top = kLowest, sum = nan_scale(sc, units);
+  float sum = nan_scale(sc, units);
 #pragma unroll
   for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -291,26 +292,41 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
     __builtin_amdgcn_s_setprio(0);
   };
   // Weights of the scores, after the running maximum moved on and outputs with it where it had to.
-  auto weights = [&](const f32x16& st, w8 (&w)[2]) {
+  // A weight is 2^(score * c - less), less being the row's reference until some row of the wave stands far from 0.  From
+  // then on every step comes by a block aside, where scores leave the reference, which stays in LDS, behind.  Measured
+  // against no such block: 16,002 rows the same, 8,000 rows of 32 heads of 128 525 and 520 us, of 16 of 64 179 and 181;
+  // with the block in line and its results chosen between in every step 530 and 185.
+  float less = kLowest;
+  uint64_t far = 0;   // lanes whose rows stand far from 0
+  auto reference = [&] { return far ? far_top[wave * 32 + col] : less; };
+  auto weights = [&](f32x16& st, w8 (&w)[2]) {
     float mx = st[0];
 #pragma unroll
     for (int e = 1; e < 16; ++e) mx = __builtin_fmaxf(mx, st[e]);
-    mx = max_halves(mx) * c;
-    if (__any(ahead<W>(mx, top))) {
-      const float next = next_reference<W>(mx, top), keep = __builtin_amdgcn_exp2f(top - next);
-      top = next;
+    mx = max_halves(mx);
+    if (__builtin_expect((__ballot(__builtin_fmaf(mx, c, -less) > kLead<W> + kLag<W>) | far) != 0, 0)) {
+      const float last = reference(), next = next_reference<W>(product(mx, c), last);
+      const float keep = __builtin_amdgcn_exp2f(last - next);
       sum *= keep;
 #pragma unroll
       for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[d][e] *= keep;
+      far = __ballot(stands_far(next));
+      less = far ? 0.0f : next;
+      if (__builtin_expect(far != 0, 0)) {
+        far_top[wave * 32 + col] = next;
+        // c is at least 2^22 / 2^128 here, so that differences over it are finite; their error is 2^-23 of 15 at most
+#pragma unroll
+        for (int e = 0; e < 16; ++e) st[e] = (product(st[e], c) - next) / c;
+      }
     }
     u32x4 pk[2];
     float add = 0;
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {
-      const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e], c, -top));
-      const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e + 1], c, -top));
+      const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e], c, -less));
+      const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e + 1], c, -less));
       add += w0;
       add += w1;
       // The weights' one rounding, to the type of the second product: matrix units bound this kernel, and a second
@@ -457,7 +473,7 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
     return;
   }
 
-  const float vs = F8 ? a.c.v_scale[item.head] : 1.0f;
+  const float vs = F8 ? a.c.v_scale[item.head] : 1.0f, top = reference();
   const uint32_t su = __builtin_bit_cast(uint32_t, sum);
   const auto sw = __builtin_amdgcn_permlane32_swap(su, su, false, false);
   const float total = __builtin_bit_cast(float, uint32_t(sw[0])) + __builtin_bit_cast(float, uint32_t(sw[1]));

@@ -48,6 +48,12 @@ __device__ __forceinline__ float product(float score, float c) {
   return score * c;
 }
 
+// Prompts' scores meet the scale inside a fused multiply-add: the error at the reference is then one that all of a row's
+// weights share, and a quarter of a power of two at most while the reference is no larger than this.  Past it they take
+// rounded products.
+constexpr float kFar = 4194304.0f;
+__device__ __forceinline__ bool stands_far(float ref) { return __builtin_fabsf(ref) > kFar && ref != kLowest; }
+
 // First value of a row's sum: NaN where scores are, as with a scale that is NaN and a row that sees a position.
 // (Kernels take the scale's magnitude from a maximum with the smallest number, which drops a NaN.)
 __device__ __forceinline__ float nan_scale(float scale, const Units& units) {
