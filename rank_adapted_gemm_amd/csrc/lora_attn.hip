@@ -316,9 +316,10 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
       less = far ? 0.0f : next;
       if (__builtin_expect(far != 0, 0)) {
         far_top[wave * 32 + col] = next;
-        // c is at least 2^22 / 2^128 here, so that differences over it are finite; their error is 2^-23 of 15 at most
+        // c is at least 2^22 / 2^128 here, so that differences over it are finite; they are off by 2^-22 of 15 at most
+        const float over_c = __builtin_amdgcn_rcpf(c);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) st[e] = (product(st[e], c) - next) / c;
+        for (int e = 0; e < 16; ++e) st[e] = behind(st[e], c, next) * over_c;
       }
     }
     u32x4 pk[2];
@@ -508,7 +509,7 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
       const u32x4 v = {uint32_t(r0[0]), uint32_t(r1[0]), uint32_t(r0[1]), uint32_t(r1[1])};
       if (m < m1) *reinterpret_cast<u32x4*>(dst + (d * 32 + e * 8 + hh * 8) * 2) = v;
     }
-  if (a.lse && hh == 0 && m < m1) a.lse[row] = total == 0 ? -INFINITY : top + __builtin_log2f(total);
+  if (a.totals && hh == 0 && m < m1) store_total(a, row, top, total);
 }
 
 template <typename T, bool F8, bool F4 = false>

@@ -53,6 +53,9 @@ __device__ __forceinline__ float product(float score, float c) {
 // rounded products.
 constexpr float kFar = 4194304.0f;
 __device__ __forceinline__ bool stands_far(float ref) { return __builtin_fabsf(ref) > kFar && ref != kLowest; }
+__device__ __forceinline__ float behind(float score, float c, float ref) {
+  return stands_far(ref) ? product(score, c) - ref : __builtin_fmaf(score, c, -ref);
+}
 
 // First value of a row's sum: NaN where scores are, as with a scale that is NaN and a row that sees a position.
 // (Kernels take the scale's magnitude from a maximum with the smallest number, which drops a NaN.)
@@ -264,10 +267,16 @@ __device__ __forceinline__ void load8(const char* p, float (&f)[8]) {
   for (int e = 0; e < 8; ++e) f[e] = float(x[e]);
 }
 
+// What the weights' pass takes off a row's scores: its reference and the logarithm of its sum, apart, since far from 0
+// their sum would lose the second.  A row that sees nothing gives no weight.
+__device__ __forceinline__ void store_total(const AttnArgs& a, int64_t row, float top, float total) {
+  reinterpret_cast<f32x2*>(a.totals)[row] = total == 0 ? f32x2{INFINITY, 0} : f32x2{top, __builtin_log2f(total)};
+}
+
 // One packed row m over units [u0, u0 + nu) of its tile, by one wave, without matrix products: a
 // score a lane, then a column (or few) a lane.  It only adds what the row sees, whatever the cache
 // holds elsewhere.  Writes the row's output, or its partial sums to `slot` where that is not negative,
-// and its maximum and sum to `ml_slot` or, there negative, their logarithm to lse.
+// and its maximum and sum to `ml_slot` or, there negative, to the rows' totals.
 template <typename T, bool F8, int DIM, bool F4 = false>
 __device__ void slow_row(const AttnArgs& a, const AttnSeq& sq, const Pages& pages, const Units& units, int u0, int nu,
                          int unit_len, int t0, int head, int m, int64_t slot, int64_t ml_slot) {
@@ -338,7 +347,7 @@ __device__ void slow_row(const AttnArgs& a, const AttnSeq& sq, const Pages& page
   }
   if (lane == 0) {
     if (ml_slot >= 0) *reinterpret_cast<f32x2*>(a.part_ml + ml_slot * 2) = f32x2{top, sum};
-    else if (a.lse) a.lse[row] = sum == 0 ? -INFINITY : top + __builtin_log2f(sum);
+    else if (a.totals) store_total(a, row, top, sum);
   }
 }
 

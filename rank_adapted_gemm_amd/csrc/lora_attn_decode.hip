@@ -342,7 +342,7 @@ __global__ __launch_bounds__(256) void join_few_kernel(AttnArgs a, AttnPart part
     const int64_t row = int64_t(sq.q_start + j) * a.heads + (m - j * a.group) + item.head * a.group;
     *reinterpret_cast<u32x2*>(a.out + (row * DIM + d) * 2) =
         u32x2{pack_pair<T>(sum[0] * inv, sum[1] * inv), pack_pair<T>(sum[2] * inv, sum[3] * inv)};
-    if (a.lse && d == 0) a.lse[row] = total == 0 ? -INFINITY : top + __builtin_log2f(total);
+    if (a.totals && d == 0) store_total(a, row, top, total);
   }
 }
 
@@ -394,7 +394,7 @@ __device__ __forceinline__ void join_one(const AttnArgs& a, const AttnSeq& sq, i
       x[e] = (acc[0][2 * tid + e] + acc[1][2 * tid + e] + acc[2][2 * tid + e] + acc[3][2 * tid + e]) * inv;
     *reinterpret_cast<uint32_t*>(a.out + (row * DIM + 2 * tid) * 2) = pack_pair<T>(x[0], x[1]);
   }
-  if (a.lse && tid == 0) a.lse[row] = total == 0 ? -INFINITY : top + __builtin_log2f(total);
+  if (a.totals && tid == 0) store_total(a, row, top, total);
 }
 
 // Many splits: a block a row.

@@ -57,7 +57,13 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_mass_ke
   const int p0 = b0 + (wave & 1) * 32, p = p0 + col;
   const Pages pages = pages_of(a, sq.index, t0, sq.kv_len - 1);
 
-  // keys: lane's position, 8 of its dimensions a product
+  const float sc = a.scale * kLog2e * (F8 ? a.c.k_scale[head] : 1.0f);
+  const uint32_t flip = sc < 0 ? 0x80008000u : 0u;
+  const float c = uniform(__builtin_fmaxf(__builtin_fabsf(sc), 1.17549435e-38f));
+  // keys: lane's position, 8 of its dimensions a product; which eight, in what order and of what sign, as in the rows'
+  // attention, so that scores are the very same numbers (matrix units round a sum and its negative differently)
+  auto chunk_of = [](int x) { return F8 ? (x >> 1) * 4 | (x & 1) : x * 2; };   // the first half of the lanes' 16 bytes of q
+  constexpr int HALF = F8 ? 2 : 1;                                             // how far on the others' lie
   x8 k[KS];
   bool bad = false;
   {
@@ -70,11 +76,12 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_mass_ke
                                        int64_t(head) * a.c.head_stride;
 #pragma unroll
     for (int x = 0; x < KS; ++x) {
-      const char* src = a.c.k + off + (x * 16 + hh * 8) * (F8 ? 1 : 2);
+      const int d = (chunk_of(x) + hh * HALF) * 8;
+      const char* src = a.c.k + off + d * (F8 ? 1 : 2);
       u32x4 v = {0, 0, 0, 0};
       if (page >= 0) {
         if constexpr (F4) {
-          const int64_t at = off + x * 8 + hh * 4;
+          const int64_t at = off + d / 2;
           v = __builtin_bit_cast(u32x4, from_e2m1<T>(*reinterpret_cast<const uint32_t*>(a.c.k + at), scale_of(a.c.k_exp[at >> 4])));
         } else if constexpr (F8) {
           const u32x2 w = *reinterpret_cast<const u32x2*>(src);
@@ -83,11 +90,10 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_mass_ke
           v = *reinterpret_cast<const u32x4*>(src);
         }
       }
-      k[x] = __builtin_bit_cast(x8, v);
+      k[x] = __builtin_bit_cast(x8, v ^ flip);
     }
   }
   const bool anybad = __any(bad);
-  const float c = uniform(a.scale * kLog2e * (F8 ? a.c.k_scale[head] : 1.0f));
 
   // A step's first packed row m is row j and head h of the group; the n-th after it lies over(h + n) rows on.
   const uint32_t group = a.group, magic = uint32_t(((uint64_t(1) << 32) + group - 1) / group);
@@ -117,22 +123,25 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_mass_ke
   auto total = [&](int m) {
     const int row = qg * QW + (lane & (QW - 1));
     const uint32_t n = h + uint32_t(min(row, m1 - 1 - m)), dj = over(n);
-    const float v = a.lse[int64_t(sq.q_start + int(j + dj)) * a.heads + int(n - dj * group) + head * int(group)];
-    return m + row < m1 && v != -INFINITY ? v : INFINITY;   // a row that sees nothing gives no weight
+    const f32x2 v = reinterpret_cast<const f32x2*>(
+        a.totals)[int64_t(sq.q_start + int(j + dj)) * a.heads + int(n - dj * group) + head * int(group)];
+    return m + row < m1 ? v : f32x2{INFINITY, 0};
   };
 
   f32x16 acc;
+  const uint32_t qbase = uint32_t((qg * QW + col) * Q::kBytes + ((hh * HALF ^ Q::key_swizzle(col)) << 4));
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0;
-  const uint32_t qbase = uint32_t((qg * QW + col) * Q::kBytes + ((hh ^ Q::key_swizzle(col)) << 4));
-  float next = INFINITY;
+  f32x2 next = {INFINITY, 0};
   if (m0 < m1) {
     issue(m0, 0);
     next = total(m0);
   }
   for (int m = m0, buf = 0; m < m1; m += QN, buf ^= 1) {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" : "+v"(next) : : "memory");
-    const uint32_t lu = __builtin_bit_cast(uint32_t, next);
+    // A row's reference and logarithm go as one number, off by 2^-12 at most, and past references of 2^12 one after the other.
+    const f32x2 rt = next;
+    const bool apart = __any(__builtin_fabsf(rt[0]) > 4096.0f && rt[0] != INFINITY);
     const int tj = t0 + int(j);
     const uint32_t th = h;
     auto time_of = [&](int n) { return tj + int(over(th + uint32_t(min(n, m1 - 1 - m)))); };   // position of row m + n
@@ -141,7 +150,13 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_mass_ke
       issue(m + QN, buf ^ 1);
       next = total(m + QN);
     }
-    const auto both = __builtin_amdgcn_permlane32_swap(lu, lu, false, false);   // rows 0 - 31 and 32 - 63 to either half
+    // rows 0 - 31 and 32 - 63 to either half
+    auto halves = [](float x) {
+      const uint32_t u = __builtin_bit_cast(uint32_t, x);
+      const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+      return f32x2{__builtin_bit_cast(float, uint32_t(r[0])), __builtin_bit_cast(float, uint32_t(r[1]))};
+    };
+    const f32x2 both = halves(rt[0] + rt[1]);
 #pragma unroll
     for (int half = 0; half < QW / 32; ++half) {
       const int na = qg * QW + half * 32, ma = m + na;
@@ -152,10 +167,11 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_mass_ke
 #pragma unroll
       for (int e = 0; e < 16; ++e) st[e] = 0;
       const uint32_t qa = lds0 + buf * TILE + half * 32 * Q::kBytes + qbase;
-      auto nth = [](int n) { return KS > 8 ? (n >> 1) | (n & 1) << 3 : n; };
+      auto nth = [](int n) { return !F8 && KS > 8 ? (n >> 1) | (n & 1) << 3 : n; };
       auto read = [&](int n) {
         typedef __attribute__((address_space(3))) const u32x4* kp;
-        return *kp(uintptr_t((qa ^ uint32_t((nth(n) & 7) * 32)) + (nth(n) >> 3) * 256));
+        const int chunk = chunk_of(nth(n));
+        return *kp(uintptr_t((qa ^ uint32_t((chunk & 15) * 16)) + (chunk >> 4) * 256));
       };
       u32x4 f[AHEAD];
 #pragma unroll
@@ -167,14 +183,20 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_mass_ke
         st = mfma32<T>(k[nth(x)], q, st);
       }
       sched_pipeline<AHEAD, KS, 1, 1>();
-      const float l = __builtin_bit_cast(float, half == 0 ? uint32_t(both[0]) : uint32_t(both[1]));
-      const bool masked = anybad || !(p0 + 31 <= ta && p0 + 31 < b1 &&
+      float l = both[half];
+      const bool masked = anybad || apart || !(p0 + 31 <= ta && p0 + 31 < b1 &&
                                       (a.window < 0 || p0 >= tb - a.window + 1 || p0 + 31 < a.sinks));
       if (masked) {
         // a row past the last sees nothing; a position past the cache lies behind every row
         const int t = ma + col < m1 ? time_of(na + col) : -1;
         const int low = a.window < 0 ? 0 : t - a.window + 1;
         const int pl = p0 + hh * 4;
+        if (apart) {
+          const float ref = halves(rt[0])[half], over_c = __builtin_amdgcn_rcpf(c);
+          l = halves(rt[1])[half];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) st[e] = behind(st[e], c, ref) * over_c;
+        }
         if (anybad) {
 #pragma unroll
           for (int e = 0; e < 16; ++e)

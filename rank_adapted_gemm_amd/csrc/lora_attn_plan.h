@@ -29,7 +29,7 @@ struct AttnPlan {
   int decode_rows;             // packed rows of the tallest decoded sequence
   int decode_tile;             // rows of a decode tile: 16 or 32
   bool inside[kAttnParts];     // the last item of a row joins it, without a launch
-  size_t off_lse, off_ml, off_scores, off_arrived, off_o, bytes;
+  size_t off_totals, off_ml, off_scores, off_arrived, off_o, bytes;
 };
 
 // A sequence's work for one kernel.
@@ -313,8 +313,8 @@ inline void attn_plan(AttnPlan& o, const KvView& c, const KvSeqs& s, int n_heads
     }
   }
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  o.off_lse = 0;
-  o.off_ml = mass && np > 0 ? up(size_t(s.q_start[s.n]) * n_heads * 4) : 0;
+  o.off_totals = 0;
+  o.off_ml = mass && np > 0 ? up(size_t(s.q_start[s.n]) * n_heads * 8) : 0;
   o.off_scores = o.off_ml + up(rows_ml * 8);
   o.off_arrived = o.off_scores + up(score);
   o.off_o = o.off_arrived + up(arrived);

@@ -174,7 +174,8 @@ struct AttnArgs {
   char* out;
   const float* mass_in;
   float* mass_out;
-  float* lse;            // workspace: per (row, head), base 2 (prompts with accumulated weights), or NULL
+  float* totals;         // workspace: per (row, head) the reference and the logarithm of the sum, base 2 (prompts with
+                         // accumulated weights), or NULL
   float* part_o;         // workspace: unnormalised output rows of split items
   float* part_ml;        // workspace: their maximum and sum
   float* scores;         // workspace: scaled scores of decode items (accumulated weights), or NULL; an item's

@@ -348,7 +348,7 @@ lora_status lora_attn(const lora_kv_cache* cache, const lora_kv_batch* batch,
   char* ws = static_cast<char*>(workspace);
   a.table = batch->page_table;
   a.table_stride = batch->table_stride;
-  a.lse = nullptr;
+  a.totals = nullptr;
   a.arrived = nullptr;
   a.call = 0;
   a.part_ml = reinterpret_cast<float*>(ws + plan.off_ml);
@@ -377,7 +377,7 @@ lora_status lora_attn(const lora_kv_cache* cache, const lora_kv_batch* batch,
     else if (e == hipSuccess && p.split_items > 0 && !inside)
       e = lora::launch_attn_join(a, p, plan.decode_tile, plan.decode.join_rows[i], dtype, stream);
   }
-  a.lse = mass_out ? reinterpret_cast<float*>(ws + plan.off_lse) : nullptr;
+  a.totals = mass_out ? reinterpret_cast<float*>(ws + plan.off_totals) : nullptr;
   for (int i = 0; i < plan.prompt.parts && e == hipSuccess; ++i) {
     lora::AttnPart& p = plan.prompt.part[i];
     e = lora::launch_attn_prompt(a, p, dtype, cache->dtype, stream);

@@ -195,3 +195,26 @@ def test_prompts_of_dense_scores(dim, cache, dtype, magnitude):
 @pytest.mark.parametrize("cache", [None, "e2m1"])
 def test_prompts_split_over_items(cache, dtype):
     check(problem(29, [40], [5000], 4, 1, 128, dtype, cache), 1.1 * 2.0 ** 30, most_unclear=0.05)
+
+
+@kinds
+@pytest.mark.parametrize("rows,lens,window,sinks", [([40], [240], -1, 0), ([70, 1], [90, 200], 50, 3)])
+def test_weights_of_prompts_with_ties(rows, lens, window, sinks, cache, dtype, magnitude):
+    p = with_ties(magnitude, rows, lens, cache, dtype)
+    for lead in (1.3, 1.77):
+        check(p, lead * 2.0 ** (magnitude - 8), window, sinks, weights=True)
+
+
+@kinds
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_weights_of_prompts_of_dense_scores(dim, cache, dtype, magnitude):
+    """The weights' pass meets the very scores that the rows' totals are of."""
+    p, scale = dense(magnitude, [48], [300], dim, cache, dtype)
+    for factor in (1.0, -1.37):
+        check(p, factor * scale, most_unclear=0.05, weights=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("cache", [None, "e2m1"])
+def test_weights_of_prompts_split_over_items(cache, dtype):
+    check(problem(29, [40], [5000], 4, 1, 128, dtype, cache), 1.1 * 2.0 ** 30, most_unclear=0.05, weights=True)
