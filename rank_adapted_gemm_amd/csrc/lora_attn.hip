@@ -466,18 +466,18 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
     ++it;
   }
 
-  if (again) {
-    for (int m = mw; m < min(m1, mw + 32); ++m)
-      slow_row<T, F8, DIM, F4>(a, sq, pages, units, u0, nu, kBN, t0, item.head, m,
-                           sq.nsplit > 1 ? int64_t(blockIdx.x) * BM + (m - m0) : -1,
-                           sq.nsplit > 1 ? int64_t(blockIdx.x) * BM + (m - m0) : -1);
-    return;
-  }
-
   const float vs = F8 ? a.c.v_scale[item.head] : 1.0f, top = reference();
   const uint32_t su = __builtin_bit_cast(uint32_t, sum);
   const auto sw = __builtin_amdgcn_permlane32_swap(su, su, false, false);
   const float total = __builtin_bit_cast(float, uint32_t(sw[0])) + __builtin_bit_cast(float, uint32_t(sw[1]));
+  if (again) {
+    for (int m = mw; m < min(m1, mw + 32); ++m)
+      slow_row<T, F8, DIM, F4>(a, sq, pages, units, u0, nu, kBN, t0, item.head, m,
+                           sq.nsplit > 1 ? int64_t(blockIdx.x) * BM + (m - m0) : -1,
+                           sq.nsplit > 1 ? int64_t(blockIdx.x) * BM + (m - m0) : -1, __shfl(top, m - mw), __shfl(total, m - mw));
+    return;
+  }
+
   if (sq.nsplit > 1) {
     if (m >= m1) return;
     const int64_t slot = int64_t(blockIdx.x) * BM + (m - m0);

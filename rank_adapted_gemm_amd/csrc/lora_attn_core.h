@@ -275,11 +275,13 @@ __device__ __forceinline__ void store_total(const AttnArgs& a, int64_t row, floa
 
 // One packed row m over units [u0, u0 + nu) of its tile, by one wave, without matrix products: a
 // score a lane, then a column (or few) a lane.  It only adds what the row sees, whatever the cache
-// holds elsewhere.  Writes the row's output, or its partial sums to `slot` where that is not negative,
-// and its maximum and sum to `ml_slot` or, there negative, to the rows' totals.
+// holds elsewhere.  Writes the row's output, or its partial sums to `slot` where that is not negative.
+// ref, total: the row's reference and sum over these units by matrix products, which the values have no part in.
+// They go to `ml_slot` or, there negative, to the rows' totals, and partial sums are brought to them: the weights of
+// positions are made of scores by matrix products, which far from 0 are other numbers than scores added up here.
 template <typename T, bool F8, int DIM, bool F4 = false>
 __device__ void slow_row(const AttnArgs& a, const AttnSeq& sq, const Pages& pages, const Units& units, int u0, int nu,
-                         int unit_len, int t0, int head, int m, int64_t slot, int64_t ml_slot) {
+                         int unit_len, int t0, int head, int m, int64_t slot, int64_t ml_slot, float ref, float total) {
   constexpr int EB = F8 ? 1 : 2, PER = DIM / 64;
   const int lane = threadIdx.x & 63;
   const int j = m / a.group, t = t0 + j, h = m - j * a.group + head * a.group;
@@ -340,14 +342,14 @@ __device__ void slow_row(const AttnArgs& a, const AttnSeq& sq, const Pages& page
     }
   }
   const int64_t row = int64_t(sq.q_start + j) * a.heads + h;
-  const float inv = sum == 0 ? 0.0f : (F8 ? a.c.v_scale[head] : 1.0f) / sum;
+  const float inv = sum == 0 ? 0.0f : (F8 ? a.c.v_scale[head] : 1.0f) / sum, share = sum == 0 ? 0.0f : total / sum;
   for (int e = 0; e < PER; ++e) {
-    if (slot >= 0) a.part_o[slot * DIM + e * 64 + lane] = acc[e];
+    if (slot >= 0) a.part_o[slot * DIM + e * 64 + lane] = acc[e] * share;
     else reinterpret_cast<T*>(a.out)[row * DIM + e * 64 + lane] = T(acc[e] * inv);
   }
   if (lane == 0) {
-    if (ml_slot >= 0) *reinterpret_cast<f32x2*>(a.part_ml + ml_slot * 2) = f32x2{top, sum};
-    else if (a.totals) store_total(a, row, top, sum);
+    if (ml_slot >= 0) *reinterpret_cast<f32x2*>(a.part_ml + ml_slot * 2) = f32x2{ref, total};
+    else if (a.totals) store_total(a, row, ref, total);
   }
 }
 

@@ -197,6 +197,29 @@ __device__ __forceinline__ void join_many(const AttnArgs& a, const AttnSeq& sq, 
   clear_arrived(a, sq, arrived);
 }
 
+// A row's reference and sum over the waves, in LDS for the block.
+template <int QT>
+__device__ __forceinline__ void meet_totals(float (&ml)[kDecodeWaves][QT * 16][2], const float (&top)[QT], const float (&total)[QT]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int x = 0; x < QT; ++x) {
+    if (lane >= 16) continue;
+    ml[wave][x * 16 + lane][0] = top[x];
+    ml[wave][x * 16 + lane][1] = total[x];
+  }
+  __syncthreads();
+}
+
+template <int ROWS>
+__device__ __forceinline__ void row_of_waves(const float (&ml)[kDecodeWaves][ROWS][2], int m, float& best, float& total) {
+  best = ml[0][m][0];
+#pragma unroll
+  for (int y = 1; y < kDecodeWaves; ++y) best = __builtin_fmaxf(best, ml[y][m][0]);
+  total = 0;
+#pragma unroll
+  for (int y = 0; y < kDecodeWaves; ++y) total += ml[y][m][1] * __builtin_amdgcn_exp2f(ml[y][m][0] - best);
+}
+
 // The waves' rows meet in LDS, WAVE_LDS bytes a wave, in RUNS runs of their columns, and leave for the output, or where they
 // were split for the workspace.
 template <typename T, int DIM, int QT, bool MASS, int WAVE_LDS, int RUNS = 1, bool MANY = false>

@@ -279,10 +279,14 @@ __global__ __launch_bounds__(kWaves * 64, decode_blocks(DIM, F8 ? 1 : 2, QT * 16
     again |= __any(!(__builtin_fabsf(any) < INFINITY) && total[x] == total[x]) != 0;
   }
   if (__syncthreads_or(again)) {
-    for (int m = wave; m < M; m += kWaves)
+    meet_totals<QT>(ml, top, total);
+    for (int m = wave; m < M; m += kWaves) {
+      float ref, sum_of_row;
+      row_of_waves(ml, m, ref, sum_of_row);
       slow_row<T, F8, DIM>(a, sq, pages, units, u0, nu, kStep, t0, item.head, m,
                            sq.nsplit > 1 ? int64_t(blockIdx.x) * BM + m : -1,
-                           sq.nsplit > 1 || MASS ? int64_t(blockIdx.x) * BM + m : -1);
+                           sq.nsplit > 1 || MASS ? int64_t(blockIdx.x) * BM + m : -1, ref, sum_of_row);
+    }
     if constexpr (!MASS) {
       __threadfence();   // rows of slow_row lie in this XCD's L2
       if (a.arrived && sq.nsplit > 1)
