@@ -255,7 +255,13 @@ def kv_append(cache, batch, k, v, rope=None, positions=None, q=None, q_out=None,
 
     With a ``rope`` keys are rotated on the way, and the batch's queries ``q`` (rows, heads, head_dim; rows and
     heads may be strided), where they are given, into ``q_out``, which is returned.  ``positions``: int32
-    (rows,) or (axes, rows); without them a row's position in its sequence, on every axis."""
+    (rows,) or (axes, rows); without them a row's position in its sequence, on every axis.
+
+    kv_append(cache, batch, k, v, stream) is the call without a rope on that stream."""
+    if rope is not None and not isinstance(rope, Rope):
+        if stream is not None:
+            raise TypeError(f"rope must be a Rope, not {type(rope).__name__}")
+        rope, stream = None, rope
     _check_batch(cache, batch)
     code = _row_code(cache, batch, "k", k)
     strides = _strides3("k", k, cache.head_dim)

@@ -155,6 +155,9 @@ class Library:
         return lambda *a: (self.calls.append((name, a)), 0)[1]
 
 
+HANDLE = at._handle
+
+
 @pytest.fixture
 def setup(monkeypatch):
     turning = at.Rope(32, axis=[0] * 8 + [1] * 8, device="cpu")
@@ -205,6 +208,31 @@ def test_rotations_arguments_go_with_a_rotation(setup):
     turning._index = 3
     with pytest.raises(ValueError):
         at.kv_append(c, b, rows[:, :2], rows[:, 2:], turning)
+    assert not lib.calls
+
+
+def test_a_stream_may_follow_the_rows(setup, monkeypatch):
+    """kv_append(cache, batch, k, v, stream), as before there were rotations."""
+    lib, c, b, turning, rows = setup
+    streams = []
+    monkeypatch.setattr(at, "_handle", lambda stream, cache: streams.append(stream) or 0)
+    side = object()
+    assert at.kv_append(c, b, rows[:, :2], rows[:, 2:], side) is None
+    at.kv_append(c, b, rows[:, :2], rows[:, 2:], None, stream=side)
+    assert [n for n, _ in lib.calls] == ["lora_kv_append"] * 2 and streams == [side, side]
+    with pytest.raises(TypeError):
+        at.kv_append(c, b, rows[:, :2], rows[:, 2:], side, stream=side)
+    with pytest.raises(ValueError):
+        at.kv_append(c, b, rows[:, :2], rows[:, 2:], side, q=rows)
+    assert len(lib.calls) == 2
+
+
+def test_what_is_neither_a_rope_nor_a_stream_is_refused(setup, monkeypatch):
+    lib, c, b, turning, rows = setup
+    monkeypatch.setattr(at, "_handle", HANDLE)
+    for wrong in (7, "side", rows):
+        with pytest.raises(TypeError):
+            at.kv_append(c, b, rows[:, :2], rows[:, 2:], wrong)
     assert not lib.calls
 
 
