@@ -54,8 +54,9 @@ class KVCache:
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         import torch
-        kinds = {torch.bfloat16: "bf16", torch.float16: "f16", torch.float8_e4m3fn: "e4m3", torch.uint8: "e2m1",
-                 torch.float4_e2m1fn_x2: "e2m1"}
+        kinds = {torch.bfloat16: "bf16", torch.float16: "f16", torch.float8_e4m3fn: "e4m3", torch.uint8: "e2m1"}
+        pairs, exponents = (getattr(torch, name, torch.uint8) for name in ("float4_e2m1fn_x2", "float8_e8m0fnu"))
+        kinds[pairs] = "e2m1"   # where torch has the type
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in kinds:
             raise ValueError("k and v must be (n_pages, page_size, kv_heads, head_dim) of one type: bfloat16, "
                              "float16, float8_e4m3fn, or uint8 of two 4-bit codes")
@@ -77,7 +78,7 @@ class KVCache:
                                          not s.is_contiguous()):
                 raise ValueError(f"{name} must be {self.kv_heads} contiguous float32 values")
             if self.dtype == "e2m1" and (
-                    s.dtype not in (torch.uint8, torch.float8_e8m0fnu) or s.dim() != 4 or
+                    s.dtype not in (torch.uint8, exponents) or s.dim() != 4 or
                     s.shape[:3] != k.shape[:3] or s.shape[3] * 32 != self.head_dim or s.stride(3) != 1 or
                     any(s.shape[i] > 1 and s.stride(i) * 16 != strides[i] for i in range(3))):
                 raise ValueError(f"{name} must be (n_pages, page_size, kv_heads, head_dim / 32) exponents (uint8 or "

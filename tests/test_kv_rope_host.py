@@ -263,6 +263,16 @@ def test_caches_in_4_bits_refuse_wrong_exponents(monkeypatch):
             at.KVCache(k, k, e, bad)
 
 
+def test_caches_need_no_types_of_newer_torch(monkeypatch):
+    monkeypatch.setattr(bd, "_check_operands", lambda *a: None)
+    monkeypatch.delattr(torch, "float4_e2m1fn_x2")
+    monkeypatch.delattr(torch, "float8_e8m0fnu")
+    k = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16)
+    assert at.KVCache(k, k).dtype == "bf16"
+    codes, exps = torch.zeros(4, 16, 2, 64, dtype=torch.uint8), torch.zeros(4, 16, 2, 4, dtype=torch.uint8)
+    assert at.KVCache(codes, codes, exps, exps).dtype == "e2m1"
+
+
 # ---------------------------------------------------------------- the reference against independent forms
 
 def test_reference_codes_are_the_nearest():
