@@ -171,6 +171,40 @@ def test_keys_that_are_not_numbers(rows, length, window, sinks, back, exp, dtype
     assert (np.abs(got - want) <= tol)[same].all()
 
 
+@pytest.mark.parametrize("rows,length,back", [(1, 200, 5), (3, 90, 33), (1, 4000, 70), (50, 180, 20), (90, 90, 1)])
+def test_infinite_keys(rows, length, back):
+    """An infinite key gives a score of either sign: rows where it is positive are NaN, and to the others its position
+    gives nothing."""
+    p = Problem4(5, [rows], [length], 4, 2, 128, 16)
+    pos = length - rows - back if rows < length else 1
+    ref = p.reference()
+    at = int(p.table[0, pos // 16]), pos % 16
+    p.ke[at[0], at[1], 0, 2] = 254
+    p.k[at[0], at[1], 0, 32:48] = 0
+    p.k[at[0], at[1], 0, 32] = 0x07                     # dimension 64: 6 times 2^127
+    c, b = p.make()
+    y = values(ra.attn(c, b, p.q))
+    q, n = values(p.q), np.arange(length)
+    table = p.table.cpu().numpy()
+    k, v = (x[table[0, n // 16], n % 16] for x in p.pool_values())
+    k[pos, 0, 64] = 0
+    for j in range(rows):
+        t = length - rows + j
+        for h in range(4):
+            sees = h < 2 and t >= pos
+            assert q[j, h, 64] != 0
+            if sees and q[j, h, 64] > 0:
+                assert np.isnan(y[j, h]).all()
+                y[j, h] = ref["out"][j, h]
+                continue
+            seen = (n <= t) & (n != pos) if sees else n <= t
+            s = k[seen, h // 2] @ q[j, h] * 128 ** -0.5
+            w = np.exp(s - s.max())
+            w /= w.sum()
+            ref["out"][j, h], ref["absv"][j, h] = w @ v[seen, h // 2], w @ np.abs(v[seen, h // 2])
+    check_out(torch.from_numpy(y), ref, "bf16", 128)
+
+
 @pytest.mark.parametrize("rows,lens", [([1, 1, 1], [500, 90, 40]), ([4, 2, 3], [300, 104, 99]), ([33, 80, 5], [200, 120, 70])])
 def test_weights_of_rows_that_need_an_invalid_page(rows, lens):
     """NaN at the positions that those rows see; every other position's weight as without it."""

@@ -275,6 +275,33 @@ def test_another_stream():
     assert torch.equal(z, q)
 
 
+def test_frequencies_outlive_a_rope_that_is_dropped():
+    """A Rope may go while a call of another stream still waits to read its frequencies: their memory is not given to what
+    is allocated next."""
+    p = Problem(43, [60, 1], [60, 300], 4, 2, 128, 16)
+    c, b = p.make()
+    want = ra.kv_append(c, b, p.new_k, p.new_v, ra.Rope(128), q=p.q)
+    k = p.k.clone()
+    at = [(int(p.table[i, t // 16]), t % 16) for i, n in enumerate(p.rows) for t in range(p.kv_len[i] - n, p.kv_len[i])]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    busy = torch.full((4096, 4096), 1e-3, device="cuda")
+    for _ in range(3):
+        p.k.zero_()
+        rope = ra.Rope(128)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                busy = (busy @ busy).clamp(-1e-3, 1e-3)
+        got = ra.kv_append(c, b, p.new_k, p.new_v, rope, q=p.q, stream=side)
+        del rope
+        others = [torch.full((64,), -1, dtype=torch.int64, device="cuda") for _ in range(64)]   # the frequencies' size
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        assert all(bool((x == -1).all()) for x in others)
+        assert all(torch.equal(p.k[x], k[x]) for x in at)
+
+
 def test_rotation_by_zero_changes_nothing():
     for dtype in ("bf16", "f16"):
         p = problem(9, [20], [20], 3, 1, 128, 16, dtype, "same")

@@ -248,6 +248,20 @@ def test_frequencies_outlive_the_calls_of_other_streams(setup, monkeypatch):
     assert noted == ["side", None]
 
 
+def test_frequencies_are_noted_for_the_stream_that_reads_them(setup, monkeypatch):
+    lib, c, b, turning, rows = setup
+    noted = []
+    monkeypatch.setattr(turning, "_turns", SimpleNamespace(record_stream=noted.append))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: ("current", device))
+    monkeypatch.setattr(at, "_handle", lambda stream, cache: 7)
+    at.kv_append(c, b, rows[:, :2], rows[:, 2:], turning, stream="side")
+    at.kv_append(c, b, rows[:, :2], rows[:, 2:], turning)
+    assert noted == ["side", ("current", turning._index)]
+    monkeypatch.setattr(at, "_handle", lambda stream, cache: turning._home)
+    at.kv_append(c, b, rows[:, :2], rows[:, 2:], turning)
+    assert len(noted) == 2
+
+
 def test_caches_in_4_bits_refuse_wrong_exponents(monkeypatch):
     monkeypatch.setattr(bd, "_check_operands", lambda *a: None)
     k = torch.zeros(4, 16, 2, 64, dtype=torch.uint8)
