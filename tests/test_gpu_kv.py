@@ -108,6 +108,16 @@ def test_evict(lens, kv, dim, page, budget, sinks, recent, cache):
     check_evict(p, mass, budget, sinks, recent)
 
 
+@pytest.mark.parametrize("kv", [1, 2, 3, 8])
+@pytest.mark.parametrize("budget", [64, 448, 512, 513, 576, 960, 1024])
+def test_evict_of_neighbouring_heads(budget, kv):
+    """64-wide e4m3 heads inside slots, two a line: any number of runs of 64 rows, full eights of them or not."""
+    lens = [budget + 40, 70, budget - 1]
+    p = evict_problem(7, lens, kv, 64, 32, budget, "e4m3")
+    mass = torch.rand(3, kv, budget + 40, device="cuda", generator=torch.Generator(device="cuda").manual_seed(budget))
+    check_evict(p, mass, budget, 3, 9)
+
+
 def test_evict_ties_and_special_weights():
     lens = [400, 400, 400, 400]
     p = evict_problem(6, lens, 1, 64, 16, 50)
