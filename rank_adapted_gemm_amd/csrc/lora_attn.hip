@@ -294,8 +294,8 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
   // Weights of the scores, after the running maximum moved on and outputs with it where it had to.
   // A weight is 2^(score * c - less), less being the row's reference until some row of the wave stands far from 0.  From
   // then on every step comes by a block aside, where scores leave the reference, which stays in LDS, behind.  Measured
-  // against no such block: 16,002 rows the same, 8,000 rows of 32 heads of 128 525 and 520 us, of 16 of 64 179 and 181;
-  // with the block in line and its results chosen between in every step 530 and 185.
+  // against no such block: within half a percent (16,002 rows of 256-wide heads; 8,000 of 32 heads of 128 502 and 501 us, of
+  // 16 of 64 175 and 176); with the block in line and its results chosen between in every step 2% more at narrow heads.
   float less = kLowest;
   uint64_t far = 0;   // lanes whose rows stand far from 0
   auto reference = [&] { return far ? far_top[wave * 32 + col] : less; };
@@ -466,11 +466,14 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
     ++it;
   }
 
-  const float vs = F8 ? a.c.v_scale[item.head] : 1.0f, top = reference();
-  const uint32_t su = __builtin_bit_cast(uint32_t, sum);
-  const auto sw = __builtin_amdgcn_permlane32_swap(su, su, false, false);
-  const float total = __builtin_bit_cast(float, uint32_t(sw[0])) + __builtin_bit_cast(float, uint32_t(sw[1]));
+  // of the lane's row, over its two lanes
+  auto row_total = [&] {
+    const uint32_t u = __builtin_bit_cast(uint32_t, sum);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __builtin_bit_cast(float, uint32_t(r[0])) + __builtin_bit_cast(float, uint32_t(r[1]));
+  };
   if (again) {
+    const float top = reference(), total = row_total();
     for (int m = mw; m < min(m1, mw + 32); ++m)
       slow_row<T, F8, DIM, F4>(a, sq, pages, units, u0, nu, kBN, t0, item.head, m,
                            sq.nsplit > 1 ? int64_t(blockIdx.x) * BM + (m - m0) : -1,
@@ -478,6 +481,7 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
     return;
   }
 
+  const float vs = F8 ? a.c.v_scale[item.head] : 1.0f, top = reference(), total = row_total();
   if (sq.nsplit > 1) {
     if (m >= m1) return;
     const int64_t slot = int64_t(blockIdx.x) * BM + (m - m0);

@@ -119,12 +119,12 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_mass_ke
       dma16_from(src, lds0 + buf * TILE + (wave * LOADS + x) * 1024);
     }
   };
+  const f32x2* totals = reinterpret_cast<const f32x2*>(a.totals) + int64_t(sq.q_start) * a.heads + head * int(group);
   // the wave's rows' totals: of row qg * QW + lane of the step
   auto total = [&](int m) {
     const int row = qg * QW + (lane & (QW - 1));
     const uint32_t n = h + uint32_t(min(row, m1 - 1 - m)), dj = over(n);
-    const f32x2 v = reinterpret_cast<const f32x2*>(
-        a.totals)[int64_t(sq.q_start + int(j + dj)) * a.heads + int(n - dj * group) + head * int(group)];
+    const f32x2 v = totals[(j + dj) * uint32_t(a.heads) + n - dj * group];
     return m + row < m1 ? v : f32x2{INFINITY, 0};
   };
 
