@@ -49,7 +49,8 @@
  * sums over positions and accumulated weights are fp32; out is rounded once at
  * the store.  Before they meet v, decoded rows' weights are split into two
  * numbers of q's type, which hold twice its bits; prompts' weights are rounded
- * once, to q's type, or to fp16 over an E4M3 cache.
+ * once, to q's type, or to fp16 over an E4M3 cache.  Scores of any size within fp32 serve: those of equal fp32
+ * value share a row's weight, which adds up to 1 in out and in the accumulated weights.
  *
  * Blocks of 4 bits.  An E2M1 cache holds the OCP microscaling format MXFP4: codes of
  * 0, 0.5, 1, 1.5, 2, 3, 4 and 6 with a sign, two a byte, the lower dimension in the low
@@ -145,8 +146,9 @@ lora_status lora_kv_append(const lora_kv_cache* cache, const lora_kv_batch* batc
  *
  * and scales it by `factor`; dimensions from `dim` on stay as they are.  One axis is a text's position;
  * several are those of images and video (time, height, width), each frequency with its own.
- * Angles are exact: a frequency is held as a fraction of a turn in 64 bits, whose product with a
- * position is reduced before anything is rounded, so the largest positions lose nothing. */
+ * Large positions lose nothing: a frequency is held as a fraction of a turn in 64 bits, whose product with
+ * a position is reduced before it is rounded.  What is left of a turn is cut to 2^-32 of one, and within an
+ * eighth of a turn from the next quarter is an fp32 number; sine and cosine are good to 2^-23. */
 typedef struct lora_rope {
   const uint64_t* turns;      /* device, dim / 2: lora_rope_turns of the frequencies */
   const uint8_t* axis;        /* HOST, dim / 2, each below n_axes; NULL: axis 0 */
@@ -159,8 +161,8 @@ typedef struct lora_rope {
   float factor;               /* finite; 1 unless a scaling of positions has one */
 } lora_rope;
 
-/* turns[j] = round(2^64 * f_j / (2 pi)) modulo 2^64 for n frequencies in radians a position; HOST arrays.
- * LORA_EINVAL for one that is not finite. */
+/* turns[j] = 2^64 * f_j / (2 pi), rounded, modulo 2^64 for n frequencies in radians a position; HOST arrays.
+ * Off by at most 1/2 + |f_j| / pi, since f_j / (2 pi) is taken in 64 bits.  LORA_EINVAL for one that is not finite. */
 lora_status lora_rope_turns(const double* freqs, int32_t n, uint64_t* turns);
 
 /*

@@ -13,7 +13,9 @@ constexpr int kAttnCUs = 256;
 // 482 rows or 2,000, riding against not: chats of 200 - 700 positions, 0.7 steps a CU, 60 against 72 us; 12 of
 // about 950, 5.8 steps a CU, 35 against 39 (64-wide heads) and 115 against 147 (128, weights); six of up to
 // 8,019, 8 steps a CU, 182 against 166 (128, e4m3) and 76 against 78 (64); 24 of about 1,000, 12 steps a CU, 115
-// against 76 (128, e4m3).
+// against 76 (128, e4m3).  Those are 16-bit and e4m3 pages.  Over e2m1 pages decoding is about twice as fast, so that the
+// limit, which is the same there, is too high: three short chats, 0.4 - 0.7 steps a CU, 140 against 151 (256) and 162
+// against 156 (128); 12 of 950, 5.6 steps, 134 against 100 (128), 2.8 steps, 129 against 100 (256) and 56 both ways (64).
 constexpr int kAttnRideUnits = 6 * kAttnCUs;
 constexpr int kAttnParts = (LORA_MAX_SEGMENTS + kAttnSeqs - 1) / kAttnSeqs;
 
@@ -269,7 +271,8 @@ inline void attn_plan(AttnPlan& o, const KvView& c, const KvSeqs& s, int n_heads
                                                   : decode_blocks(c.dim, cache_dtype == LORA_KV_E4M3 ? 1 : 2, o.decode_tile);
   // Over e2m1 pages a unit is a quarter as long, so that starts and joins count for more of them: with the bytes above,
   // one stream of 8,019 positions, 8 heads of 128, was cut into 125 items a head and took 29 us, with these 13.5; six
-  // chats of 256-wide heads 31 both ways, 64 streams 140.
+  // chats of 256-wide heads 31 both ways, 64 streams 140.  The numbers are fitted to those, which have tiles of 16 rows;
+  // tiles of 32, whose sums are twice as many bytes, have the same.
   const int64_t dslots = dblocks * kAttnCUs;
   const int dchunk = cache_dtype == LORA_KV_E2M1
                          ? attn_chunk(dec, nd, c.kv_heads, dslots, 12, 1, 6, 0.2, 2, 0)
