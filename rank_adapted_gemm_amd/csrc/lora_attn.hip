@@ -316,8 +316,8 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_kernel(
       less = far ? 0.0f : next;
       if (__builtin_expect(far != 0, 0)) {
         far_top[wave * 32 + col] = next;
-        // c is at least 2^22 / 2^128 here, so that differences over it are finite; they are off by 2^-22 of 15 at most
-        const float over_c = __builtin_amdgcn_rcpf(c);
+        // c is at least 2^22 / 2^128 here, so that differences over it are finite; they are off by 2^-23 of 15 at most
+        const float over_c = 1.0f / c;   // a small number past 2^126, which the reciprocal instruction would make 0
 #pragma unroll
         for (int e = 0; e < 16; ++e) st[e] = behind(st[e], c, next) * over_c;
       }

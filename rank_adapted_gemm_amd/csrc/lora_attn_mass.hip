@@ -192,7 +192,7 @@ __global__ __launch_bounds__(kWaves * 64, DIM == 64 ? 4 : 2) void prompt_mass_ke
         const int low = a.window < 0 ? 0 : t - a.window + 1;
         const int pl = p0 + hh * 4;
         if (apart) {
-          const float ref = halves(rt[0])[half], over_c = __builtin_amdgcn_rcpf(c);
+          const float ref = halves(rt[0])[half], over_c = 1.0f / c;
           l = halves(rt[1])[half];
 #pragma unroll
           for (int e = 0; e < 16; ++e) st[e] = behind(st[e], c, ref) * over_c;

@@ -243,3 +243,17 @@ def test_weights_beside_values_that_are_not_numbers(rows, lens, dim, cache, dtyp
     """Rows that see an infinite or NaN value are gone over one by one, which must not touch their weights."""
     p, scale = dense(magnitude, rows, lens, dim, cache, dtype)
     check(p, scale, most_unclear=0.05, weights=True, spoiled=37)
+
+
+@pytest.mark.parametrize("rows,lens", [([1], [310]), ([40], [240])])
+@pytest.mark.parametrize("cache", [None, "e2m1"])
+def test_scales_near_the_largest_number(cache, rows, lens):
+    """Far scores of small queries and keys, under a scale whose reciprocal is below the normal numbers."""
+    p = with_ties(30, rows, lens, cache, "bf16")
+    p.q *= 2.0 ** -50
+    if cache:
+        p.ke[p.ke != 255] -= 52
+    else:
+        p.k *= 2.0 ** -52
+    for lead in (1.3, 1.9):
+        check(p, lead * 2.0 ** 126, weights=True)
